@@ -33,6 +33,7 @@ __all__ = [
     "gemm_nvfp4_w4a4_grouped_packed", "nvfp4_quantize_bf16", "nvfp4_quantize_bf16_routed",
     "nvfp4_fp4_fallback",
     "nvfp4_node_exec", "moe_route", "moe_permute_rows", "moe_combine", "GroupedSchedule",
+    "gemm_int8_w8a8", "gemm_int8_w8a8_grouped",
     "C_FUNCTIONS",
 ]
 
@@ -41,12 +42,14 @@ class Fmt(enum.IntEnum):
     BF16 = 0
     FP8_E4M3 = 1
     NVFP4 = 2
+    INT8 = 3
 
 
 class Kind(enum.IntEnum):
     BF16_MMA = 0
     FP8_MMA = 1
     FP4_BLOCK_SCALED = 2
+    INT8_MMA = 3
     INVALID = -1
 
 
@@ -56,6 +59,7 @@ class Exec(enum.IntEnum):
     BF16_WIDEN = 2
     NO_FP4_KERNEL = 3
     NO_PATH = 4
+    INT8_MMA = 5
 
 
 class Op(enum.IntEnum):
@@ -68,6 +72,8 @@ class Op(enum.IntEnum):
     W4A4_PACKED = 5
     QUANTIZE = 6
     MOE_ROUTE = 7
+    INT8 = 8
+    INT8_GROUPED = 9
 
 
 class Status(enum.IntEnum):
@@ -133,6 +139,8 @@ C_FUNCTIONS = {
     "nvfp4_quantize_bf16": (_I, [_P, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
     "nvfp4_quantize_bf16_noalloc": (_I, [_P, _I, _I, _P, _P, _P, _P, _P]),
     "nvfp4_quantize_bf16_routed": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
+    "gemm_int8_w8a8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "gemm_int8_w8a8_grouped": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P]),
 }
 
 _lock = threading.Lock()
@@ -743,3 +751,68 @@ class GroupedSchedule:
             pa, sA_packed.data_ptr(), pw, sW_packed.data_ptr(), self.buf.data_ptr(), self.E,
             self.M, psrc, pwt, py, int(T), self.N, self.K, _stream_ptr(stream)))
         return out
+
+
+# --- INT8 products ------------------------------------------------------------------
+
+def _on(dev, stream):
+    """The context a call of the INT8 path runs in: the tensors' device is current, and
+    what the call allocates belongs to the stream that uses it."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
+    """Y[M,N] (bf16) = sA[m] * sW[n] * A . W^T: INT8 codes A [M,K], W [N,K] with one
+    float32 scale per token (sA [M]) and per output channel (sW [N]); exact INT32 sums
+    (K a multiple of 16, at most 131056)."""
+    torch = _torch()
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise TypeError("A and W must be 2-D torch.Tensors")
+    M, K = A.shape
+    N = W.shape[0]
+    pa = _dev_tensor(A, torch.int8, (M, K), "A")
+    psa = _dev_tensor(sA, torch.float32, (M,), "sA")
+    pw = _dev_tensor(W, torch.int8, (N, K), "W")
+    psw = _dev_tensor(sW, torch.float32, (N,), "sW")
+    _same_device(A.device, sA=sA, W=W, sW=sW, out=out)
+    with _on(A.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        py = _dev_tensor(out, torch.bfloat16, (M, N), "out")
+        _err(load_library().gemm_int8_w8a8(pa, psa, pw, psw, py, M, N, K, _stream_ptr(stream)))
+    return out
+
+
+def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
+    """The experts' INT8 products: rows offsets[e] .. offsets[e+1]-1 of A (INT8 [M,K], sA
+    float32 [M]) times W[e] (INT8 [E,N,K], sW float32 [E,N]).  offsets: CUDA int32 [E+1]
+    as moe_route returns it, read on the device.  Rows from offsets[E] on are not written."""
+    torch = _torch()
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise TypeError("A must be a 2-D and W a 3-D torch.Tensor")
+    M, K = A.shape
+    E, N = W.shape[0], W.shape[1]
+    pa = _dev_tensor(A, torch.int8, (M, K), "A")
+    psa = _dev_tensor(sA, torch.float32, (M,), "sA")
+    pw = _dev_tensor(W, torch.int8, (E, N, K), "W")
+    psw = _dev_tensor(sW, torch.float32, (E, N), "sW")
+    po = _dev_tensor(offsets, torch.int32, (E + 1,), "offsets")
+    _same_device(A.device, sA=sA, W=W, sW=sW, offsets=offsets, out=out)
+    with _on(A.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        py = _dev_tensor(out, torch.bfloat16, (M, N), "out")
+        _err(load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K,
+                                                   _stream_ptr(stream)))
+    return out

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -26,6 +27,7 @@
 #include "grouped_pair_kernel.cuh"
 #include "quantize_kernel.cuh"
 #include "moe_kernel.cuh"
+#include "int8_kernel.cuh"
 
 namespace {
 
@@ -103,6 +105,7 @@ bool class_has_fp8_mma(int arch) { return arch >= 89; }
 bool class_compiles_fp4_kernel(int arch) { return arch == 100; }
 bool class_compiles_fp8_exact_kernel(int arch) { return arch == 100; }
 bool class_compiles_bf16_widen_kernel(int arch) { return arch == 100; }
+bool class_compiles_int8_kernel(int arch) { return arch == 100; }
 
 // fp4_fallback: an NVFP4 activation on a class without an FP4 block-scale
 // kernel.  NoFp4Kernel where the class's tensor cores do FP4 but this library
@@ -115,7 +118,8 @@ nvfp4_exec fp4_fallback(int arch) {
 }
 
 bool valid_fmt(nvfp4_fmt f) {
-    return f == NVFP4_FMT_BF16 || f == NVFP4_FMT_FP8_E4M3 || f == NVFP4_FMT_NVFP4;
+    return f == NVFP4_FMT_BF16 || f == NVFP4_FMT_FP8_E4M3 || f == NVFP4_FMT_NVFP4 ||
+           f == NVFP4_FMT_INT8;
 }
 
 // Launch-time check shared by the W4A4 entry points.
@@ -280,13 +284,16 @@ nvfp4_kind nvfp4_kind_of(nvfp4_fmt activation) {
     case NVFP4_FMT_BF16: return NVFP4_KIND_BF16_MMA;
     case NVFP4_FMT_FP8_E4M3: return NVFP4_KIND_FP8_MMA;
     case NVFP4_FMT_NVFP4: return NVFP4_KIND_FP4_BLOCK_SCALED;
+    case NVFP4_FMT_INT8: return NVFP4_KIND_INT8_MMA;
     }
     return NVFP4_KIND_INVALID;
 }
 
 const char* nvfp4_pair_name(nvfp4_fmt weight, nvfp4_fmt activation) {
-    static const char* names[3][3] = {
-        {"W16A16", "W16A8", "W16A4"}, {"W8A16", "W8A8", "W8A4"}, {"W4A16", "W4A8", "W4A4"}};
+    static const char* names[4][4] = {{"W16A16", "W16A8", "W16A4", "W16A8I"},
+                                      {"W8A16", "W8A8", "W8A4", "W8A8I"},
+                                      {"W4A16", "W4A8", "W4A4", "W4A8I"},
+                                      {"W8IA16", "W8IA8", "W8IA4", "W8IA8I"}};
     if (!valid_fmt(weight) || !valid_fmt(activation)) return "?";
     return names[weight][activation];
 }
@@ -298,6 +305,7 @@ const char* nvfp4_exec_name(nvfp4_exec e) {
     case NVFP4_EXEC_BF16_WIDEN: return "BF16_WIDEN";
     case NVFP4_EXEC_NO_FP4_KERNEL: return "NO_FP4_KERNEL";
     case NVFP4_EXEC_NO_PATH: return "NO_PATH";
+    case NVFP4_EXEC_INT8_MMA: return "INT8_MMA";
     }
     return "?";
 }
@@ -305,7 +313,10 @@ const char* nvfp4_exec_name(nvfp4_exec e) {
 nvfp4_exec nvfp4_exec_of_arch(int arch, nvfp4_fmt weight, nvfp4_fmt activation,
                               int fp4_kernel_disabled) {
     if (!valid_fmt(weight) || !valid_fmt(activation)) return NVFP4_EXEC_NO_PATH;
-    if (weight != NVFP4_FMT_NVFP4) return NVFP4_EXEC_NO_PATH;  // NVFP4-weight paths only
+    if (weight == NVFP4_FMT_INT8)
+        return activation == NVFP4_FMT_INT8 && class_compiles_int8_kernel(arch) ? NVFP4_EXEC_INT8_MMA
+                                                                                : NVFP4_EXEC_NO_PATH;
+    if (weight != NVFP4_FMT_NVFP4) return NVFP4_EXEC_NO_PATH;  // no BF16- or FP8-weight paths
     switch (nvfp4_kind_of(activation)) {
     case NVFP4_KIND_FP4_BLOCK_SCALED:
         if (class_has_fp4_mma(arch) && class_compiles_fp4_kernel(arch) && !fp4_kernel_disabled)
@@ -357,7 +368,7 @@ nvfp4_status nvfp4_check_device_error(void* stream) {
         return fail(NVFP4_ERR_DEVICE_TIMEOUT, "a kernel wait expired (role %d)", (v >> 8) & 0xFF);
     if (v & nvfp4::grouped_pair::BAD_OFFSETS)
         return fail(NVFP4_ERR_INVALID_ARG,
-                    "device expert offsets were not a non-decreasing run from 0 to M");
+                    "device expert offsets were not a non-decreasing run from 0 to M (INT8: to at most M)");
     if (v & nvfp4::grouped_pair::BAD_DEST)
         return fail(NVFP4_ERR_INVALID_ARG, "a grouped row's output row (src) was outside [0, T)");
     return fail(NVFP4_ERR_INVALID_ARG, "a routed expert id was outside [0, E)");
@@ -1301,6 +1312,122 @@ nvfp4_status gemm_nvfp4_w4a4_grouped(const uint8_t* A, const uint8_t* sA, float 
                                 nullptr, 0, stream);
 }
 
+// ------------------------------------------------------------------------- INT8
+namespace {
+// How an INT8 product runs: on pairs or single SMs, the tile's token columns, the CTAs
+// that share a tile's K range, the stages and the grid.
+struct Int8Plan {
+    bool pair = false;
+    nvfp4::int8::Shape shape{};
+    long long tiles = 0;  // an upper bound (the token blocks are known on the device only)
+    int grid = 0;
+    size_t smem = 0;
+};
+
+constexpr size_t kInt8SmemMax = 227 * 1024;
+constexpr size_t kInt8SmemTwo = 113 * 1024;  // two CTAs fit one SM
+
+Int8Plan int8_plan(int M, int N, int K, int E, int num_sms) {
+    namespace i8 = nvfp4::int8;
+    Int8Plan p;
+    const int nk = (K + i8::BKB - 1) / i8::BKB;
+    const int avg = (int)(((long long)M + E - 1) / E);  // rows of an expert, on average
+    auto blocks = [&](int bt) { return std::min<long long>(M, M / bt + std::min(E, M)); };
+    int bt, split = 1;
+    p.pair = avg > 256;
+    if (p.pair) {
+        bt = i8::MAX_BT;
+        p.tiles = blocks(bt) * ((N + 2 * i8::BW - 1) / (2 * i8::BW));
+    } else {
+        const long long want = E == 1 ? M : 2ll * avg;
+        bt = (int)std::min<long long>((want + 15) / 16 * 16, i8::MAX_BT);
+        p.tiles = blocks(bt) * ((N + i8::BW - 1) / i8::BW);
+        const int slots = bt <= 128 ? 2 * num_sms : num_sms;
+        while (split < i8::MAX_SPLIT && p.tiles * split * 2 <= slots && split * 8 <= nk) split *= 2;
+    }
+    const size_t budget = !p.pair && split > 1 && bt <= 128 ? kInt8SmemTwo : kInt8SmemMax;
+    int stages = 2;
+    while (stages < i8::MAX_STAGES && i8::smem_bytes(p.pair, bt, split, stages + 1) <= budget) ++stages;
+    p.shape = {M, N, K, E, bt, split, stages};
+    p.smem = i8::smem_bytes(p.pair, bt, split, stages);
+    const int per = p.pair ? 2 : split;
+    long long clusters = p.tiles;
+    if (split == 1) clusters = std::min<long long>(clusters, num_sms / per);
+    p.grid = (int)std::min<long long>(clusters * per, 1ll << 30);
+    return p;
+}
+
+nvfp4_status launch_int8(const int8_t* A, const float* sA, const int8_t* W, const float* sW,
+                         const int32_t* offsets, int E, void* Y, int M, int N, int K, void* stream) {
+    namespace i8 = nvfp4::int8;
+    if (M < 0 || N < 0) return fail(NVFP4_ERR_INVALID_ARG, "M and N must be >= 0 (got %d, %d)", M, N);
+    if (K < 16 || K % 16 != 0 || K > i8::MAX_K)
+        return fail(NVFP4_ERR_INVALID_ARG, "INT8 needs K a multiple of 16 in [16, %d] (got %d)",
+                    i8::MAX_K, K);
+    if ((long long)E * N > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "E * N too large");
+    if (M > 0 && N > 0) {
+        if (!A || !sA || !W || !sW || !Y) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned16(A) || !aligned16(W) || !aligned16(Y))
+            return fail(NVFP4_ERR_MISALIGNED, "A, W and Y must be 16-byte aligned");
+        if (reinterpret_cast<uintptr_t>(sA) % 4 != 0 || reinterpret_cast<uintptr_t>(sW) % 4 != 0 ||
+            reinterpret_cast<uintptr_t>(offsets) % 4 != 0)
+            return fail(NVFP4_ERR_MISALIGNED, "sA, sW and offsets must be 4-byte aligned");
+    }
+    int dev;
+    DevInfo info;
+    if (!current_device(dev, info)) return fail(NVFP4_ERR_CUDA, "cannot query the current CUDA device");
+    if (nvfp4_exec_of_arch(info.sm_arch, NVFP4_FMT_INT8, NVFP4_FMT_INT8, 0) != NVFP4_EXEC_INT8_MMA)
+        return fail(NVFP4_ERR_NOPATH, "no INT8 kernel is compiled for sm_%d", info.sm_arch);
+    if (M == 0 || N == 0) return ok();
+
+    const Int8Plan p = int8_plan(M, N, K, E, info.num_sms);
+    if (p.tiles > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "M x N too large");
+    nvfp4_status st;
+    CUtensorMap tmW, tmA;
+    if ((st = make_map_u8(&tmW, W, (uint64_t)K, (uint64_t)E * N, i8::BKB, i8::BW)) != NVFP4_OK) return st;
+    if ((st = make_map_u8(&tmA, A, (uint64_t)K, (uint64_t)M, i8::BKB,
+                          (uint32_t)(p.pair ? p.shape.bt / 2 : p.shape.bt))) != NVFP4_OK)
+        return st;
+    auto kern = p.pair ? i8::int8_kernel<true> : i8::int8_kernel<false>;
+    // the attribute's ceiling is the same on every call: calls of other host threads may
+    // sit between setting it and launching
+    if ((st = set_smem(kern, kInt8SmemMax, info, "int8_kernel")) != NVFP4_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.grid);
+    cfg.blockDim = dim3(i8::NUM_THREADS);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    // may start while the stream's previous kernel finishes (see grid_dependency_wait)
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)(p.pair ? 2 : p.shape.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmW, tmA, sA, sW, offsets,
+                                       reinterpret_cast<__nv_bfloat16*>(Y), p.shape);
+    if (e != cudaSuccess) return cuda_fail(e, "launching int8_kernel");
+    return ok();
+}
+}  // namespace
+
+nvfp4_status gemm_int8_w8a8(const int8_t* A, const float* sA, const int8_t* W, const float* sW,
+                            void* Y, int M, int N, int K, void* stream) {
+    return launch_int8(A, sA, W, sW, nullptr, 1, Y, M, N, K, stream);
+}
+
+nvfp4_status gemm_int8_w8a8_grouped(const int8_t* A, const float* sA, const int8_t* W,
+                                    const float* sW, const int32_t* offsets_dev, int E, int total_M,
+                                    void* Y, int N, int K, void* stream) {
+    if (E < 1 || E > nvfp4::int8::MAX_EXPERTS)
+        return fail(NVFP4_ERR_INVALID_ARG, "E must be in [1, %d] (got %d)", nvfp4::int8::MAX_EXPERTS, E);
+    if (!offsets_dev) return fail(NVFP4_ERR_INVALID_ARG, "null offsets");
+    return launch_int8(A, sA, W, sW, offsets_dev, E, Y, total_M, N, K, stream);
+}
+
 // ------------------------------------------------------------------------- generic queries
 size_t nvfp4_workspace_size(int op, int M, int N, int K, int E) {
     switch (op) {
@@ -1308,6 +1435,8 @@ size_t nvfp4_workspace_size(int op, int M, int N, int K, int E) {
         case NVFP4_OP_VIA_FP8:
         case NVFP4_OP_W4A16:
         case NVFP4_OP_W4A8:
+        case NVFP4_OP_INT8:
+        case NVFP4_OP_INT8_GROUPED:
             return 0;
         case NVFP4_OP_W4A4_GROUPED: {
             GroupedWs w;

@@ -65,7 +65,8 @@ typedef enum {
 typedef enum {
     NVFP4_FMT_BF16 = 0,
     NVFP4_FMT_FP8_E4M3 = 1,
-    NVFP4_FMT_NVFP4 = 2
+    NVFP4_FMT_NVFP4 = 2,
+    NVFP4_FMT_INT8 = 3             /* signed 8-bit codes, one FP32 scale per row */
 } nvfp4_fmt;
 
 /* The MMA kind an activation format needs (`kind_of`). */
@@ -73,6 +74,7 @@ typedef enum {
     NVFP4_KIND_BF16_MMA = 0,       /* BF16 activations; weights widened in registers */
     NVFP4_KIND_FP8_MMA = 1,
     NVFP4_KIND_FP4_BLOCK_SCALED = 2,
+    NVFP4_KIND_INT8_MMA = 3,
     NVFP4_KIND_INVALID = -1
 } nvfp4_kind;
 
@@ -82,7 +84,8 @@ typedef enum {
     NVFP4_EXEC_FP8_EXACT = 1,      /* exact E2M1->E4M3 conversion on the FP8 MMA: gemm_nvfp4_via_fp8 (W4A4), gemm_nvfp4_w4a8 (W4A8) */
     NVFP4_EXEC_BF16_WIDEN = 2,     /* BF16 MMA, NVFP4 weights widened in registers: gemm_w4a16 */
     NVFP4_EXEC_NO_FP4_KERNEL = 3,  /* device has the FP4 MMA, but its class has no compiled kernel */
-    NVFP4_EXEC_NO_PATH = 4         /* neither native nor exact: refused, never widened */
+    NVFP4_EXEC_NO_PATH = 4,        /* neither native nor exact: refused, never widened */
+    NVFP4_EXEC_INT8_MMA = 5        /* INT8 MMA under INT8 weights: gemm_int8_w8a8 */
 } nvfp4_exec;
 
 /* ---- planning (host only, no device work) -------------------------------- */
@@ -101,8 +104,10 @@ NVFP4_API nvfp4_kind nvfp4_kind_of(nvfp4_fmt activation);
  * (NVFP4, FP8) (W4A8): no single-instruction MMA takes FP8 activations under
  * NVFP4 weights with E4M3 group-16 scales, so the exact E4M3 path: FP8_EXACT on
  * sm_100 (gemm_nvfp4_w4a8), NO_PATH on every other class.
- * Pairs whose weights are not NVFP4: NO_PATH (this library carries NVFP4-weight
- * paths only).  `fp4_kernel_disabled` != 0 behaves as if the class compiled no
+ * (INT8, INT8) (W8A8 in integers): INT8_MMA on sm_100 (gemm_int8_w8a8), NO_PATH
+ * elsewhere.
+ * Every other pair: NO_PATH (no BF16- or FP8-weight paths, and integer codes never
+ * meet floating-point ones).  `fp4_kernel_disabled` != 0 behaves as if the class compiled no
  * FP4 block-scale kernel (module doc, `fp4_fallback`, `avail::without_fp4_kernel`). */
 NVFP4_API nvfp4_exec nvfp4_exec_of_arch(int sm_arch, nvfp4_fmt weight, nvfp4_fmt activation,
                               int fp4_kernel_disabled);
@@ -130,7 +135,8 @@ NVFP4_API nvfp4_exec nvfp4_fp4_fallback(int sm_arch);
  * NVFP4_ERR_INVALID_ARG for n < 0 or a null array with n > 0; n == 0 is OK.
  * A declared format is never planned at a wider one: a node's answer is
  * FP4_MMA only for NVFP4 activations, FP8_EXACT only for NVFP4 weights under
- * NVFP4 or FP8 activations, BF16_WIDEN only for BF16 activations. */
+ * NVFP4 or FP8 activations, BF16_WIDEN only for BF16 activations, INT8_MMA only
+ * for INT8 weights and activations. */
 NVFP4_API nvfp4_status nvfp4_node_exec(int sm_arch, int fp4_kernel_disabled,
                                        const int32_t* weight_fmt, const int32_t* activation_fmt,
                                        int n, int32_t* exec_out);
@@ -546,6 +552,38 @@ NVFP4_API nvfp4_status gemm_nvfp4_w4a4_grouped_packed_sched_combine(
     const void* sched, int E, int M, const int32_t* src, const float* weights, void* Y_bf16, int T,
     int N, int K, void* stream);
 
+/* ---- INT8 products -------------------------------------------------------
+ * Y[m,n] = BF16( sA[m] * sW[n] * sum_k a[m,k] * w[n,k] )
+ *
+ * for layers kept in 8-bit integers beside the NVFP4 ones.  a, w are signed 8-bit
+ * codes, any value of -128..127; sA is one FP32 scale per token (row of A), sW one
+ * per output channel (row of W).  The sum over k is an exact INT32 sum, scaled in
+ * FP32 (one rounding each for sA*sW, the sum's conversion and their product) and
+ * rounded once to BF16, so equal inputs give equal bits on every call.
+ *
+ * A [M][K] and W [N][K] are row-major int8 and Y [M][N] bf16, 16-byte aligned; sA
+ * [M] and sW [N] are float, 4-byte aligned.  K is a multiple of 16, 16 <= K <= 131056
+ * (the INT32 sum cannot overflow); M, N >= 0 are otherwise free.  Nothing is enqueued
+ * for M == 0 or N == 0.  No workspace.  A and W may be the same buffer; Y may not
+ * overlap an input. */
+NVFP4_API nvfp4_status gemm_int8_w8a8(const int8_t* A, const float* sA, const int8_t* W,
+                                      const float* sW, void* Y_bf16, int M, int N, int K,
+                                      void* stream);
+
+/* The experts' INT8 products: rows offsets[e] .. offsets[e+1]-1 of A times W_e^T, with
+ * W [E][N][K], sW [E][N] and the rows in the order nvfp4_moe_route gives.
+ *   offsets_dev  device int32 [E+1], 4-byte aligned: offsets[0] = 0, non-decreasing,
+ *                offsets[E] <= total_M.  It is read by the kernel, so the call needs
+ *                no host round trip and can be captured in a graph.  Rows of Y from
+ *                offsets[E] on are left as they were.  Offsets that are not such a run
+ *                write nothing at all and are reported by nvfp4_check_device_error().
+ *   E            1 .. 256.  E * N must stay below 2^31.
+ * Every row's result is bit for bit gemm_int8_w8a8's of that row and expert. */
+NVFP4_API nvfp4_status gemm_int8_w8a8_grouped(const int8_t* A, const float* sA, const int8_t* W,
+                                              const float* sW, const int32_t* offsets_dev, int E,
+                                              int total_M, void* Y_bf16, int N, int K,
+                                              void* stream);
+
 /* ---- generic workspace query and scale preparation ------------------------ */
 
 /* The operations whose workspace nvfp4_workspace_size reports. */
@@ -557,7 +595,9 @@ typedef enum {
     NVFP4_OP_W4A8 = 4,          /* gemm_nvfp4_w4a8: none */
     NVFP4_OP_W4A4_PACKED = 5,   /* gemm_nvfp4_w4a4_packed_ws on the current device, all pairs */
     NVFP4_OP_QUANTIZE = 6,      /* nvfp4_quantize_bf16 (a constant) */
-    NVFP4_OP_MOE_ROUTE = 7      /* nvfp4_moe_route with num_pairs = M */
+    NVFP4_OP_MOE_ROUTE = 7,     /* nvfp4_moe_route with num_pairs = M */
+    NVFP4_OP_INT8 = 8,          /* gemm_int8_w8a8: none */
+    NVFP4_OP_INT8_GROUPED = 9   /* gemm_int8_w8a8_grouped: none */
 } nvfp4_op;
 
 /* Device bytes of caller workspace that operation `op` (an nvfp4_op) needs for
@@ -585,7 +625,8 @@ NVFP4_API const char* nvfp4_last_error(void);
  * kernel sets when one of its bounded waits expires.  NVFP4_OK if clear,
  * NVFP4_ERR_DEVICE_TIMEOUT if a wait expired, NVFP4_ERR_INVALID_ARG if the only
  * records are bad data seen on the device (an out-of-range expert id in
- * nvfp4_moe_route, bad offsets in nvfp4_grouped_schedule), NVFP4_ERR_CUDA if
+ * nvfp4_moe_route, bad offsets in nvfp4_grouped_schedule or
+ * gemm_int8_w8a8_grouped), NVFP4_ERR_CUDA if
  * synchronization failed. */
 NVFP4_API nvfp4_status nvfp4_check_device_error(void* stream);
 

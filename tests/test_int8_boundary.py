@@ -1,0 +1,64 @@
+"""INT8 entry points without a device: argument checks, the planner's answers, names."""
+import pytest
+
+import block_scaled_precision_nvfp4_b200 as nv
+
+S = nv.Status
+
+
+def test_argument_errors_need_no_device():
+    lib = nv.load_library()
+
+    def call(A=16, sA=4, W=16, sW=4, Y=16, M=4, N=4, K=64):
+        return lib.gemm_int8_w8a8(A, sA, W, sW, Y, M, N, K, None)
+    for kw in (dict(M=-1), dict(N=-1), dict(K=0), dict(K=8), dict(K=40), dict(K=-16),
+               dict(K=131072), dict(A=0), dict(sA=0), dict(W=0), dict(sW=0), dict(Y=0)):
+        assert call(**kw) == S.INVALID_ARG, kw
+    for kw in (dict(A=24), dict(W=17), dict(Y=8), dict(sA=2), dict(sW=7)):
+        assert call(**kw) == S.MISALIGNED, kw
+
+
+def test_grouped_argument_errors_need_no_device():
+    lib = nv.load_library()
+
+    def call(A=16, off=4, E=2, M=4, N=4, K=64):
+        return lib.gemm_int8_w8a8_grouped(A, 4, 16, 4, off, E, M, 16, N, K, None)
+    for kw in (dict(E=0), dict(E=257), dict(E=-1), dict(off=0), dict(M=-1), dict(N=-2), dict(K=72),
+               dict(A=0), dict(E=256, N=2 ** 23)):
+        assert call(**kw) == S.INVALID_ARG, kw
+    assert call(off=6) == S.MISALIGNED
+    assert call(A=40) == S.MISALIGNED
+
+
+def test_planner_knows_the_int8_pair():
+    F, E = nv.Fmt, nv.Exec
+    assert nv.nvfp4_kind_of(F.INT8) == nv.Kind.INT8_MMA
+    assert nv.nvfp4_exec_of_arch(100, F.INT8, F.INT8) == E.INT8_MMA
+    assert nv.nvfp4_exec_of_arch(100, F.INT8, F.INT8, fp4_kernel_disabled=True) == E.INT8_MMA
+    for arch in (80, 89, 90, 103, 120):
+        assert nv.nvfp4_exec_of_arch(arch, F.INT8, F.INT8) == E.NO_PATH
+    for f in (F.BF16, F.FP8_E4M3, F.NVFP4):   # integer codes never meet floating-point ones
+        assert nv.nvfp4_exec_of_arch(100, F.INT8, f) == E.NO_PATH
+        assert nv.nvfp4_exec_of_arch(100, f, F.INT8) == E.NO_PATH
+    assert nv.nvfp4_node_exec(100, [(F.INT8, F.INT8), (F.NVFP4, F.INT8)]) == [E.INT8_MMA, E.NO_PATH]
+
+
+def test_names():
+    F = nv.Fmt
+    assert nv.nvfp4_pair_name(F.INT8, F.INT8) == "W8IA8I"
+    assert nv.nvfp4_pair_name(F.NVFP4, F.INT8) == "W4A8I"
+    assert nv.nvfp4_pair_name(F.FP8_E4M3, F.FP8_E4M3) == "W8A8"
+    assert nv.nvfp4_exec_name(nv.Exec.INT8_MMA) == "INT8_MMA"
+    assert len({nv.nvfp4_pair_name(a, b) for a in F for b in F}) == len(F) ** 2
+
+
+@pytest.mark.parametrize("op", [nv.Op.INT8, nv.Op.INT8_GROUPED])
+def test_no_workspace(op):
+    assert nv.nvfp4_workspace_size(op, 4096, 5376, 14336, 8) == 0
+
+
+def test_cpu_tensors_are_refused():
+    import torch
+    z = lambda *s: torch.zeros(s, dtype=torch.int8)
+    with pytest.raises(ValueError):
+        nv.gemm_int8_w8a8(z(2, 32), torch.zeros(2), z(4, 32), torch.zeros(4))
