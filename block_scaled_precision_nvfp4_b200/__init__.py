@@ -33,7 +33,8 @@ __all__ = [
     "gemm_nvfp4_w4a4_grouped_packed", "nvfp4_quantize_bf16", "nvfp4_quantize_bf16_routed",
     "nvfp4_fp4_fallback",
     "nvfp4_node_exec", "moe_route", "moe_permute_rows", "moe_combine", "GroupedSchedule",
-    "gemm_int8_w8a8", "gemm_int8_w8a8_grouped",
+    "gemm_int8_w8a8", "gemm_int8_w8a8_grouped", "int8_quantize_bf16", "int8_quantize_bf16_routed",
+    "moe_topk",
     "C_FUNCTIONS",
 ]
 
@@ -74,6 +75,8 @@ class Op(enum.IntEnum):
     MOE_ROUTE = 7
     INT8 = 8
     INT8_GROUPED = 9
+    INT8_QUANTIZE = 10
+    MOE_TOPK = 11
 
 
 class Status(enum.IntEnum):
@@ -140,6 +143,9 @@ C_FUNCTIONS = {
     "nvfp4_quantize_bf16_noalloc": (_I, [_P, _I, _I, _P, _P, _P, _P, _P]),
     "nvfp4_quantize_bf16_routed": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
     "gemm_int8_w8a8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "int8_quantize_bf16": (_I, [_P, _I, _I, _P, _P, _P]),
+    "int8_quantize_bf16_routed": (_I, [_P, _I, _I, _P, _I, _P, _P, _P]),
+    "nvfp4_moe_topk": (_I, [_P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P]),
     "gemm_int8_w8a8_grouped": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P]),
 }
 
@@ -816,3 +822,87 @@ def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
         _err(load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K,
                                                    _stream_ptr(stream)))
     return out
+
+
+def _int8_quantize(x, dest, k, out, stream):
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a 2-D torch.Tensor")
+    rows, K = x.shape
+    px = _dev_tensor(x, torch.bfloat16, (rows, K), "x")
+    if dest is not None:
+        pd = _dev_tensor(dest, torch.int32, (rows * k,), "dest")
+        _same_device(x.device, dest=dest)
+    n = rows * k if dest is not None else rows
+    with _on(x.device, stream):
+        if out is None:
+            out = (torch.empty((n, K), dtype=torch.int8, device=x.device),
+                   torch.empty(n, dtype=torch.float32, device=x.device))
+        codes, scales = out
+        pc = _dev_tensor(codes, torch.int8, (n, K), "codes")
+        ps = _dev_tensor(scales, torch.float32, (n,), "scales")
+        _same_device(x.device, codes=codes, scales=scales)
+        lib, st = load_library(), _stream_ptr(stream)
+        if dest is None:
+            _err(lib.int8_quantize_bf16(px, rows, K, pc, ps, st))
+        else:
+            _err(lib.int8_quantize_bf16_routed(px, rows, K, pd, k, pc, ps, st))
+    return codes, scales
+
+
+def int8_quantize_bf16(x, out=None, stream=None):
+    """BF16 [rows, K] -> (codes int8 [rows, K], scales float32 [rows]): one scale per row,
+    amax/127 (1 for a row of zeros; NaN, with zero codes, for a row with an Inf or NaN),
+    codes = 127 x / amax rounded half to even.  K a multiple of 16.  `out`, if given, is
+    such a tuple of preallocated tensors."""
+    return _int8_quantize(x, None, 1, out, stream)
+
+
+def int8_quantize_bf16_routed(x, dest, k=1, out=None, stream=None):
+    """int8_quantize_bf16 writing token row r to rows dest[r*k + j] (j < k): the quantised
+    rows in an MoE dispatch's order.  `dest` is the int32 [rows*k] CUDA tensor moe_route
+    returns; entries outside [0, rows*k) are left out.  Returns (codes int8 [rows*k, K],
+    scales float32 [rows*k])."""
+    if dest is None:
+        raise TypeError("dest must be a torch.Tensor")
+    return _int8_quantize(x, dest, int(k), out, stream)
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_topk(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_top=2,
+             renormalize=True, scale=1.0, out=None, stream=None):
+    """Routing to experts: logits (CUDA float32 or bfloat16 [T, E]) -> (ids int32 [T, k],
+    weights float32 [T, k]), what moe_route and moe_combine take.
+
+    score: "softmax" or "sigmoid".  bias (float32 [E]) steers the choice, not the weights.
+    With groups > 1, only the top_groups groups of E/groups experts with the largest sums
+    of their group_top (1 or 2) best choices take part.  ids are in descending order of the
+    choice, ties to the lowest index; weights are the chosen scores, divided by their sum
+    if renormalize, times scale.  A NaN logit counts as -Inf."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D torch.Tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    T, E = logits.shape
+    k = int(k)
+    pl = _dev_tensor(logits, logits.dtype, (T, E), "logits")
+    pb = _dev_tensor(bias, torch.float32, (E,), "bias") if bias is not None else None
+    _same_device(logits.device, bias=bias)
+    with _on(logits.device, stream):
+        if out is None:
+            out = (torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device),
+                   torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device))
+        ids, weights = out
+        pi = _dev_tensor(ids, torch.int32, (T, k), "ids")
+        pw = _dev_tensor(weights, torch.float32, (T, k), "weights")
+        _same_device(logits.device, ids=ids, weights=weights)
+        _err(load_library().nvfp4_moe_topk(pl, int(logits.dtype == torch.bfloat16), T, E, k,
+                                           _SCORES[score], pb, int(groups), int(top_groups),
+                                           int(group_top), int(bool(renormalize)), float(scale),
+                                           pi, pw, _stream_ptr(stream)))
+    return ids, weights

@@ -28,6 +28,8 @@
 #include "quantize_kernel.cuh"
 #include "moe_kernel.cuh"
 #include "int8_kernel.cuh"
+#include "int8_quantize_kernel.cuh"
+#include "moe_topk_kernel.cuh"
 
 namespace {
 
@@ -268,6 +270,32 @@ W4a16LdgKern w4a16_ldg_kernel_for(int nb) {
         case 5: return k16::w4a16_ldg_kernel<5>;
         default: return k16::w4a16_ldg_kernel<6>;
     }
+}
+
+// A launch that may start while the stream's previous kernel finishes (the kernel waits
+// for it before it reads or writes memory).
+template <typename... P, typename... Args>
+cudaError_t launch_programmatic(void (*kern)(P...), dim3 grid, int threads, void* stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+template <typename X>
+void (*topk_kernel_for(int v))(const X*, const float*, int32_t*, float*, nvfp4::topk::Params) {
+    namespace tk = nvfp4::topk;
+    if (v <= 1) return tk::moe_topk_kernel<1, X>;
+    if (v <= 2) return tk::moe_topk_kernel<2, X>;
+    if (v <= 4) return tk::moe_topk_kernel<4, X>;
+    if (v <= 8) return tk::moe_topk_kernel<8, X>;
+    return tk::moe_topk_kernel<16, X>;
 }
 
 }  // namespace
@@ -1428,6 +1456,109 @@ nvfp4_status gemm_int8_w8a8_grouped(const int8_t* A, const float* sA, const int8
     return launch_int8(A, sA, W, sW, offsets_dev, E, Y, total_M, N, K, stream);
 }
 
+// ------------------------------------------------------------------------- INT8 quantiser
+namespace {
+nvfp4_status int8_quantize_impl(const void* X, int rows, int K, const int32_t* dest, int k,
+                                int8_t* codes, float* scales, void* stream) {
+    namespace q = nvfp4::int8q;
+    if (rows < 0) return fail(NVFP4_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+    if (K < 16 || K % 16 != 0)
+        return fail(NVFP4_ERR_INVALID_ARG, "K must be a positive multiple of 16 (got %d)", K);
+    if (rows > 0) {
+        if (!X || !codes || !scales) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned16(X) || !aligned16(codes))
+            return fail(NVFP4_ERR_MISALIGNED, "X and codes must be 16-byte aligned");
+        if (reinterpret_cast<uintptr_t>(scales) % 4 != 0 || reinterpret_cast<uintptr_t>(dest) % 4 != 0)
+            return fail(NVFP4_ERR_MISALIGNED, "scales and dest must be 4-byte aligned");
+    }
+    int dev;
+    DevInfo info;
+    if (!current_device(dev, info)) return fail(NVFP4_ERR_CUDA, "cannot query the current CUDA device");
+    if (info.sm_arch != 100)
+        return fail(NVFP4_ERR_NOPATH, "the quantiser is compiled for sm_100 only (device sm_%d)",
+                    info.sm_arch);
+    if (rows == 0) return ok();
+    // the fewest threads that hold a row in registers with at most 4 (then 8) loads each
+    auto kern = q::int8_quantize_kernel<256, 0>;
+    int tpr = 256;
+    if (K <= 32 * 32) { kern = q::int8_quantize_kernel<32, 4>; tpr = 32; }
+    else if (K <= 64 * 32) { kern = q::int8_quantize_kernel<64, 4>; tpr = 64; }
+    else if (K <= 128 * 32) { kern = q::int8_quantize_kernel<128, 4>; tpr = 128; }
+    else if (K <= 256 * 32) { kern = q::int8_quantize_kernel<256, 4>; }
+    else if (K <= 256 * 64) { kern = q::int8_quantize_kernel<256, 8>; }
+    const int rpb = q::THREADS / tpr;
+    cudaError_t e = launch_programmatic(kern, dim3((unsigned)((rows + rpb - 1) / rpb)), q::THREADS,
+                                        stream, static_cast<const uint4*>(X), rows, K, codes, scales,
+                                        dest, k);
+    if (e != cudaSuccess) return cuda_fail(e, "launching int8_quantize_kernel");
+    return ok();
+}
+}  // namespace
+
+nvfp4_status int8_quantize_bf16(const void* X, int rows, int K, int8_t* codes, float* scales,
+                                void* stream) {
+    return int8_quantize_impl(X, rows, K, nullptr, 1, codes, scales, stream);
+}
+
+nvfp4_status int8_quantize_bf16_routed(const void* X, int rows, int K, const int32_t* dest, int k,
+                                       int8_t* codes, float* scales, void* stream) {
+    if (k < 1 || k > 32) return fail(NVFP4_ERR_INVALID_ARG, "k must be in [1, 32] (got %d)", k);
+    if (rows > 0 && !dest) return fail(NVFP4_ERR_INVALID_ARG, "null dest");
+    if ((long long)rows * k > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "rows * k too large");
+    return int8_quantize_impl(X, rows, K, dest, k, codes, scales, stream);
+}
+
+// ------------------------------------------------------------------------- routing to experts
+nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, int k, int score,
+                            const float* bias, int groups, int top_groups, int group_top,
+                            int renormalize, float scale, int32_t* ids, float* weights,
+                            void* stream) {
+    namespace tk = nvfp4::topk;
+    if (T < 0) return fail(NVFP4_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+    if (E < 1 || E > tk::MAX_EXPERTS)
+        return fail(NVFP4_ERR_INVALID_ARG, "E must be in [1, %d] (got %d)", tk::MAX_EXPERTS, E);
+    if (score != NVFP4_SCORE_SOFTMAX && score != NVFP4_SCORE_SIGMOID)
+        return fail(NVFP4_ERR_INVALID_ARG, "unknown score function %d", score);
+    if (groups < 1 || groups > tk::MAX_GROUPS || E % groups != 0)
+        return fail(NVFP4_ERR_INVALID_ARG, "groups must be in [1, %d] and divide E (got %d of %d)",
+                    tk::MAX_GROUPS, groups, E);
+    if (top_groups < 1 || top_groups > groups)
+        return fail(NVFP4_ERR_INVALID_ARG, "top_groups must be in [1, groups] (got %d)", top_groups);
+    if (group_top != 1 && group_top != 2)
+        return fail(NVFP4_ERR_INVALID_ARG, "group_top must be 1 or 2 (got %d)", group_top);
+    const int per = E / groups;
+    if (k < 1 || k > tk::MAX_K || k > top_groups * per)
+        return fail(NVFP4_ERR_INVALID_ARG, "k must be in [1, %d] and at most the %d experts kept (got %d)",
+                    tk::MAX_K, top_groups * per, k);
+    if (T > 0) {
+        if (!logits || !ids || !weights) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned16(logits)) return fail(NVFP4_ERR_MISALIGNED, "logits must be 16-byte aligned");
+        if (reinterpret_cast<uintptr_t>(bias) % 4 != 0 || reinterpret_cast<uintptr_t>(ids) % 4 != 0 ||
+            reinterpret_cast<uintptr_t>(weights) % 4 != 0)
+            return fail(NVFP4_ERR_MISALIGNED, "bias, ids and weights must be 4-byte aligned");
+    }
+    int dev;
+    DevInfo info;
+    if (!current_device(dev, info)) return fail(NVFP4_ERR_CUDA, "cannot query the current CUDA device");
+    if (info.sm_arch != 100)
+        return fail(NVFP4_ERR_NOPATH, "the router is compiled for sm_100 only (device sm_%d)", info.sm_arch);
+    if (T == 0) return ok();
+    tk::Params p = {T, E, k, score == NVFP4_SCORE_SIGMOID, groups, top_groups, group_top,
+                    renormalize != 0, scale, per, 32};
+    while (p.lpg * groups > 32) p.lpg /= 2;  // a power of two of lanes for each group
+    const int v = (per + p.lpg - 1) / p.lpg;
+    const dim3 grid((unsigned)((T + tk::WARPS - 1) / tk::WARPS));
+    cudaError_t e;
+    if (logits_bf16)
+        e = launch_programmatic(topk_kernel_for<__nv_bfloat16>(v), grid, 32 * tk::WARPS, stream,
+                                static_cast<const __nv_bfloat16*>(logits), bias, ids, weights, p);
+    else
+        e = launch_programmatic(topk_kernel_for<float>(v), grid, 32 * tk::WARPS, stream,
+                                static_cast<const float*>(logits), bias, ids, weights, p);
+    if (e != cudaSuccess) return cuda_fail(e, "launching moe_topk_kernel");
+    return ok();
+}
+
 // ------------------------------------------------------------------------- generic queries
 size_t nvfp4_workspace_size(int op, int M, int N, int K, int E) {
     switch (op) {
@@ -1437,6 +1568,8 @@ size_t nvfp4_workspace_size(int op, int M, int N, int K, int E) {
         case NVFP4_OP_W4A8:
         case NVFP4_OP_INT8:
         case NVFP4_OP_INT8_GROUPED:
+        case NVFP4_OP_INT8_QUANTIZE:
+        case NVFP4_OP_MOE_TOPK:
             return 0;
         case NVFP4_OP_W4A4_GROUPED: {
             GroupedWs w;

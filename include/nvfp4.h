@@ -584,6 +584,63 @@ NVFP4_API nvfp4_status gemm_int8_w8a8_grouped(const int8_t* A, const float* sA, 
                                               int total_M, void* Y_bf16, int N, int K,
                                               void* stream);
 
+/* BF16 rows -> INT8 codes with one FP32 scale per row: a token's activations ahead of
+ * gemm_int8_w8a8, or an output channel's weights, once.
+ *
+ *     scales[r] = amax_r / 127                        (1 for a row of zeros)
+ *     codes[r,k] = round-half-to-even( 127 x / amax_r )   of the real quotient
+ *
+ * A row that holds an Inf or a NaN gets the scale NaN and zero codes (its products are
+ * NaN; other rows are not touched).  X [rows][K] bf16 and codes [rows][K] int8 are
+ * row-major and 16-byte aligned, scales [rows] float 4-byte aligned; K is a positive
+ * multiple of 16, rows >= 0.  No workspace. */
+NVFP4_API nvfp4_status int8_quantize_bf16(const void* X_bf16, int rows, int K, int8_t* codes,
+                                          float* scales, void* stream);
+
+/* int8_quantize_bf16 writing token row r's codes and scale to rows dest[r*k + j], j < k,
+ * of codes [rows*k][K] and scales [rows*k]: the rows in the order nvfp4_moe_route gives
+ * (its dest, device int32 [rows*k], 4-byte aligned; 1 <= k <= 32).  Entries outside
+ * [0, rows*k), such as the -1 of an out-of-range expert id, are left out, and rows that
+ * nothing is sent to are left as they were.  Two entries may not name one row. */
+NVFP4_API nvfp4_status int8_quantize_bf16_routed(const void* X_bf16, int rows, int K,
+                                                 const int32_t* dest, int k, int8_t* codes,
+                                                 float* scales, void* stream);
+
+/* ---- routing to experts ---------------------------------------------------
+ * From the router's logits x [T][E] to the expert ids and weights that nvfp4_moe_route
+ * and nvfp4_moe_combine take:
+ *
+ *     s_e = softmax(x)_e or 1/(1 + exp(-x_e))        (score)
+ *     c_e = s_e + bias[e]                            (bias NULL: none; choice only)
+ *     groups > 1: experts in `groups` runs of E/groups; a run's score is the sum of its
+ *         group_top (1 or 2) largest c; the top_groups best runs are kept
+ *     ids[t][j] = the k largest c of the kept runs, in descending order, j = 0..k-1
+ *     weights[t][j] = s of that expert, divided by the k scores' sum if `renormalize`
+ *         (0 where that sum is 0), times `scale`
+ *
+ * Ties go to the lowest index.  Choices are compared in 64 bits (without a bias, experts
+ * compare by their logits), so the ids are those of the formula and not of a rounding.
+ * A NaN logit counts as -Inf, +Inf as the largest finite value; a NaN choice counts as
+ * -Inf.  Experts masked by -Inf (logit or bias) are chosen only when nothing else is left
+ * in the kept groups; a logit of -Inf has the score 0, and a row with no logit above -Inf
+ * has k distinct ids and weights 0.
+ *
+ *   logits     device [T][E], contiguous: bf16 if logits_bf16 != 0, else float
+ *   bias       device float [E] or NULL
+ *   ids        device int32 [T][k]; weights device float [T][k]
+ *   E          1 .. 256; k 1 .. 32, at most top_groups * (E / groups)
+ *   groups     1 .. 32, dividing E; 1 <= top_groups <= groups
+ * logits are 16-byte aligned, the others 4-byte aligned.  No workspace; T >= 0. */
+typedef enum {
+    NVFP4_SCORE_SOFTMAX = 0,
+    NVFP4_SCORE_SIGMOID = 1
+} nvfp4_score;
+
+NVFP4_API nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, int k,
+                                      int score, const float* bias, int groups, int top_groups,
+                                      int group_top, int renormalize, float scale, int32_t* ids,
+                                      float* weights, void* stream);
+
 /* ---- generic workspace query and scale preparation ------------------------ */
 
 /* The operations whose workspace nvfp4_workspace_size reports. */
@@ -597,7 +654,9 @@ typedef enum {
     NVFP4_OP_QUANTIZE = 6,      /* nvfp4_quantize_bf16 (a constant) */
     NVFP4_OP_MOE_ROUTE = 7,     /* nvfp4_moe_route with num_pairs = M */
     NVFP4_OP_INT8 = 8,          /* gemm_int8_w8a8: none */
-    NVFP4_OP_INT8_GROUPED = 9   /* gemm_int8_w8a8_grouped: none */
+    NVFP4_OP_INT8_GROUPED = 9,  /* gemm_int8_w8a8_grouped: none */
+    NVFP4_OP_INT8_QUANTIZE = 10, /* int8_quantize_bf16, int8_quantize_bf16_routed: none */
+    NVFP4_OP_MOE_TOPK = 11      /* nvfp4_moe_topk: none */
 } nvfp4_op;
 
 /* Device bytes of caller workspace that operation `op` (an nvfp4_op) needs for

@@ -62,3 +62,38 @@ def test_cpu_tensors_are_refused():
     z = lambda *s: torch.zeros(s, dtype=torch.int8)
     with pytest.raises(ValueError):
         nv.gemm_int8_w8a8(z(2, 32), torch.zeros(2), z(4, 32), torch.zeros(4))
+
+
+def test_quantiser_argument_errors_need_no_device():
+    lib = nv.load_library()
+
+    def call(X=16, rows=4, K=64, c=16, s=4):
+        return lib.int8_quantize_bf16(X, rows, K, c, s, None)
+    for kw in (dict(rows=-1), dict(K=0), dict(K=8), dict(K=24), dict(X=0), dict(c=0), dict(s=0)):
+        assert call(**kw) == S.INVALID_ARG, kw
+    for kw in (dict(X=18), dict(c=24), dict(s=6)):
+        assert call(**kw) == S.MISALIGNED, kw
+
+    def routed(dest=4, k=2, rows=4, K=64):
+        return lib.int8_quantize_bf16_routed(16, rows, K, dest, k, 16, 4, None)
+    for kw in (dict(k=0), dict(k=33), dict(dest=0), dict(rows=2 ** 30, k=2), dict(K=40)):
+        assert routed(**kw) == S.INVALID_ARG, kw
+    assert routed(dest=2) == S.MISALIGNED
+
+
+def test_router_argument_errors_need_no_device():
+    lib = nv.load_library()
+
+    def call(x=16, bf16=0, T=4, E=16, k=2, score=0, bias=4, groups=4, top=2, gt=2, ids=4, w=4):
+        return lib.nvfp4_moe_topk(x, bf16, T, E, k, score, bias, groups, top, gt, 1, 1.0, ids, w, None)
+    for kw in (dict(T=-1), dict(E=0), dict(E=257), dict(k=0), dict(k=9), dict(k=33, E=256, groups=1, top=1),
+               dict(score=2), dict(score=-1), dict(groups=3), dict(groups=0), dict(groups=64, E=128),
+               dict(top=0), dict(top=5), dict(gt=0), dict(gt=3), dict(x=0), dict(ids=0), dict(w=0)):
+        assert call(**kw) == S.INVALID_ARG, kw
+    for kw in (dict(x=8), dict(bias=5), dict(ids=2), dict(w=1)):
+        assert call(**kw) == S.MISALIGNED, kw
+
+
+@pytest.mark.parametrize("op", [nv.Op.INT8_QUANTIZE, nv.Op.MOE_TOPK])
+def test_router_and_quantiser_need_no_workspace(op):
+    assert nv.nvfp4_workspace_size(op, 4096, 256, 14336, 8) == 0
