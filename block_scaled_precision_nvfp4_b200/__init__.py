@@ -160,6 +160,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libnvfp4_b200.so (building it with nvcc if absent).  Raises if it cannot load."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_build.LIB):
@@ -235,9 +237,15 @@ def nvfp4_exec_name(e: Exec) -> str:
 
 # --- tensor marshalling -----------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream=None) -> int:
@@ -759,23 +767,55 @@ class GroupedSchedule:
         return out
 
 
-# --- INT8 products ------------------------------------------------------------------
+# --- INT8 products, their quantiser and the router -----------------------------------
+#
+# These are called once per layer and token batch, so the marshalling is kept short: one
+# test per tensor, and the current device and stream looked up without building objects.
 
-def _on(dev, stream):
-    """The context a call of the INT8 path runs in: the tensors' device is current, and
-    what the call allocates belongs to the stream that uses it."""
+_raw = None
+
+
+def _raw_calls():
+    """(current device index, current raw stream of a device index), as plain calls."""
+    global _raw
+    if _raw is None:
+        torch = _torch()
+        c = torch._C
+        if hasattr(c, "_cuda_getDevice") and hasattr(c, "_cuda_getCurrentRawStream"):
+            _raw = (c._cuda_getDevice, c._cuda_getCurrentRawStream)
+        else:
+            _raw = (torch.cuda.current_device, lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw
+
+
+def _elsewhere(t, stream):
+    """The context a call has to enter first, or None: the tensors' device becomes current,
+    and what the call allocates belongs to the stream that uses it."""
     torch = _torch()
-    if stream is None:
-        return torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream)
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.is_cuda and t.get_device() != _raw_calls()[0]():
+        return torch.cuda.device(t.device)
+    return None
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _ptr(t, dtype, shape, name, dev):
+    """t's address; raises unless t is a contiguous `dtype` tensor of `shape` on CUDA device
+    index `dev`."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and dev >= 0
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_tensor(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on CUDA device {dev}, got {t.device}")
+
+
+def _is_matrix(t, dims=2):
+    return isinstance(t, _torch().Tensor) and t.dim() == dims
 
 
 def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
@@ -783,20 +823,21 @@ def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
     float32 scale per token (sA [M]) and per output channel (sW [N]); exact INT32 sums
     (K a multiple of 16, at most 131056)."""
     torch = _torch()
-    if not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+    if not _is_matrix(A) or not _is_matrix(W):
         raise TypeError("A and W must be 2-D torch.Tensors")
-    M, K = A.shape
-    N = W.shape[0]
-    pa = _dev_tensor(A, torch.int8, (M, K), "A")
-    psa = _dev_tensor(sA, torch.float32, (M,), "sA")
-    pw = _dev_tensor(W, torch.int8, (N, K), "W")
-    psw = _dev_tensor(sW, torch.float32, (N,), "sW")
-    _same_device(A.device, sA=sA, W=W, sW=sW, out=out)
-    with _on(A.device, stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-        py = _dev_tensor(out, torch.bfloat16, (M, N), "out")
-        _err(load_library().gemm_int8_w8a8(pa, psa, pw, psw, py, M, N, K, _stream_ptr(stream)))
+    ctx = _elsewhere(A, stream)
+    if ctx is not None:
+        with ctx:
+            return gemm_int8_w8a8(A, sA, W, sW, out)
+    (M, K), N, dev = A.shape, W.shape[0], A.get_device()
+    pa = _ptr(A, torch.int8, (M, K), "A", dev)
+    psa = _ptr(sA, torch.float32, (M,), "sA", dev)
+    pw = _ptr(W, torch.int8, (N, K), "W", dev)
+    psw = _ptr(sW, torch.float32, (N,), "sW", dev)
+    if out is None:
+        out = A.new_empty((M, N), dtype=torch.bfloat16)
+    py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
+    _err(load_library().gemm_int8_w8a8(pa, psa, pw, psw, py, M, N, K, _raw_calls()[1](dev)))
     return out
 
 
@@ -805,48 +846,48 @@ def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
     float32 [M]) times W[e] (INT8 [E,N,K], sW float32 [E,N]).  offsets: CUDA int32 [E+1]
     as moe_route returns it, read on the device.  Rows from offsets[E] on are not written."""
     torch = _torch()
-    if not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 3:
+    if not _is_matrix(A) or not _is_matrix(W, 3):
         raise TypeError("A must be a 2-D and W a 3-D torch.Tensor")
-    M, K = A.shape
-    E, N = W.shape[0], W.shape[1]
-    pa = _dev_tensor(A, torch.int8, (M, K), "A")
-    psa = _dev_tensor(sA, torch.float32, (M,), "sA")
-    pw = _dev_tensor(W, torch.int8, (E, N, K), "W")
-    psw = _dev_tensor(sW, torch.float32, (E, N), "sW")
-    po = _dev_tensor(offsets, torch.int32, (E + 1,), "offsets")
-    _same_device(A.device, sA=sA, W=W, sW=sW, offsets=offsets, out=out)
-    with _on(A.device, stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-        py = _dev_tensor(out, torch.bfloat16, (M, N), "out")
-        _err(load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K,
-                                                   _stream_ptr(stream)))
+    ctx = _elsewhere(A, stream)
+    if ctx is not None:
+        with ctx:
+            return gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out)
+    (M, K), (E, N, _), dev = A.shape, W.shape, A.get_device()
+    pa = _ptr(A, torch.int8, (M, K), "A", dev)
+    psa = _ptr(sA, torch.float32, (M,), "sA", dev)
+    pw = _ptr(W, torch.int8, (E, N, K), "W", dev)
+    psw = _ptr(sW, torch.float32, (E, N), "sW", dev)
+    po = _ptr(offsets, torch.int32, (E + 1,), "offsets", dev)
+    if out is None:
+        out = A.new_empty((M, N), dtype=torch.bfloat16)
+    py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
+    _err(load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K,
+                                               _raw_calls()[1](dev)))
     return out
 
 
 def _int8_quantize(x, dest, k, out, stream):
     torch = _torch()
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+    if not _is_matrix(x):
         raise TypeError("x must be a 2-D torch.Tensor")
-    rows, K = x.shape
-    px = _dev_tensor(x, torch.bfloat16, (rows, K), "x")
-    if dest is not None:
-        pd = _dev_tensor(dest, torch.int32, (rows * k,), "dest")
-        _same_device(x.device, dest=dest)
-    n = rows * k if dest is not None else rows
-    with _on(x.device, stream):
-        if out is None:
-            out = (torch.empty((n, K), dtype=torch.int8, device=x.device),
-                   torch.empty(n, dtype=torch.float32, device=x.device))
-        codes, scales = out
-        pc = _dev_tensor(codes, torch.int8, (n, K), "codes")
-        ps = _dev_tensor(scales, torch.float32, (n,), "scales")
-        _same_device(x.device, codes=codes, scales=scales)
-        lib, st = load_library(), _stream_ptr(stream)
-        if dest is None:
-            _err(lib.int8_quantize_bf16(px, rows, K, pc, ps, st))
-        else:
-            _err(lib.int8_quantize_bf16_routed(px, rows, K, pd, k, pc, ps, st))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return _int8_quantize(x, dest, k, out, None)
+    (rows, K), dev = x.shape, x.get_device()
+    n = rows if dest is None else rows * k
+    px = _ptr(x, torch.bfloat16, (rows, K), "x", dev)
+    pd = None if dest is None else _ptr(dest, torch.int32, (n,), "dest", dev)
+    if out is None:
+        out = (x.new_empty((n, K), dtype=torch.int8), x.new_empty((n,), dtype=torch.float32))
+    codes, scales = out
+    pc = _ptr(codes, torch.int8, (n, K), "codes", dev)
+    ps = _ptr(scales, torch.float32, (n,), "scales", dev)
+    lib, st = load_library(), _raw_calls()[1](dev)
+    if dest is None:
+        _err(lib.int8_quantize_bf16(px, rows, K, pc, ps, st))
+    else:
+        _err(lib.int8_quantize_bf16_routed(px, rows, K, pd, k, pc, ps, st))
     return codes, scales
 
 
@@ -865,7 +906,10 @@ def int8_quantize_bf16_routed(x, dest, k=1, out=None, stream=None):
     scales float32 [rows*k])."""
     if dest is None:
         raise TypeError("dest must be a torch.Tensor")
-    return _int8_quantize(x, dest, int(k), out, stream)
+    k = int(k)
+    if k < 1:
+        raise ValueError(f"k must be >= 1, got {k}")
+    return _int8_quantize(x, dest, k, out, stream)
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -882,27 +926,28 @@ def moe_topk(logits, k, score="softmax", bias=None, groups=1, top_groups=1, grou
     choice, ties to the lowest index; weights are the chosen scores, divided by their sum
     if renormalize, times scale.  A NaN logit counts as -Inf."""
     torch = _torch()
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+    if not _is_matrix(logits):
         raise TypeError("logits must be a 2-D torch.Tensor")
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    T, E = logits.shape
-    k = int(k)
-    pl = _dev_tensor(logits, logits.dtype, (T, E), "logits")
-    pb = _dev_tensor(bias, torch.float32, (E,), "bias") if bias is not None else None
-    _same_device(logits.device, bias=bias)
-    with _on(logits.device, stream):
-        if out is None:
-            out = (torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device),
-                   torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device))
-        ids, weights = out
-        pi = _dev_tensor(ids, torch.int32, (T, k), "ids")
-        pw = _dev_tensor(weights, torch.float32, (T, k), "weights")
-        _same_device(logits.device, ids=ids, weights=weights)
-        _err(load_library().nvfp4_moe_topk(pl, int(logits.dtype == torch.bfloat16), T, E, k,
-                                           _SCORES[score], pb, int(groups), int(top_groups),
-                                           int(group_top), int(bool(renormalize)), float(scale),
-                                           pi, pw, _stream_ptr(stream)))
+    ctx = _elsewhere(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_topk(logits, k, score, bias, groups, top_groups, group_top, renormalize,
+                            scale, out)
+    (T, E), k, dev = logits.shape, int(k), logits.get_device()
+    pl = _ptr(logits, logits.dtype, (T, E), "logits", dev)
+    pb = None if bias is None else _ptr(bias, torch.float32, (E,), "bias", dev)
+    if out is None:
+        out = (logits.new_empty((T, max(k, 0)), dtype=torch.int32),
+               logits.new_empty((T, max(k, 0)), dtype=torch.float32))
+    ids, weights = out
+    pi = _ptr(ids, torch.int32, (T, max(k, 0)), "ids", dev)
+    pw = _ptr(weights, torch.float32, (T, max(k, 0)), "weights", dev)
+    _err(load_library().nvfp4_moe_topk(pl, logits.dtype is torch.bfloat16, T, E, k,
+                                       _SCORES[score], pb, int(groups), int(top_groups),
+                                       int(group_top), bool(renormalize), float(scale), pi, pw,
+                                       _raw_calls()[1](dev)))
     return ids, weights
