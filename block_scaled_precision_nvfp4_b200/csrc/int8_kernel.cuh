@@ -36,7 +36,6 @@ using w4a4::ROLE_DRAIN;
 using w4a4::ROLE_EPI;
 using w4a4::ROLE_MMA;
 using w4a4::ROLE_PRODUCER;
-using w4a4::warp_wait;
 
 constexpr int MAX_EXPERTS = grouped_pair::MAX_EXPERTS;
 constexpr int BW = 128;          // weight rows (channels) per CTA
@@ -119,6 +118,41 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_
 //   bits 17-22 N >> 3              bits 24-28 M >> 4
 __host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
     return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// A stage and the parity of its barriers, advanced by one stage at a time.
+struct Ring {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// Bounded wait of a whole converged warp (mbar_wait's limit and error record).  Every lane
+// polls, so no shuffle or branch stands between the barrier and the work behind it, and
+// the clock and the abort flag are looked at once every 32 polls: a K-block of one tile of
+// 16 tokens took 0.35 us with a one-lane wait that reads the clock on every poll, 0.21 us
+// with this one.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int role) {
+    uint64_t t0 = 0;
+    bool ok = true;
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if ((n & 31) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort || now - t0 > wait_limit_ns()) {
+                if (!*abort) atomicOr(&g_device_error, 1 | (role << 8));
+                *abort = 1;
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 struct Tile {
@@ -256,15 +290,16 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
     if (warp == 0) {
         // ------------------------------------------------------------ producer (every CTA)
         int it = 0;
+        Ring ring;
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += nclusters) {
             const Tile tl = decode(sm, s, t, nblk, TILE_N);
             const int wrow = tl.e * s.N + tl.n0 + (PAIR ? (int)rank * BW : 0);
             // a pair's MMA takes the first half of its columns from CTA 0, the rest from CTA 1
             const int arow = tl.m0 + (PAIR ? (int)rank * ((tl.rows + 31) / 32 * 16) : 0);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int st = it % s.stages;
-                if (!warp_wait(&sm.empty[st], ((it / s.stages) & 1) ^ 1, abort, ROLE_PRODUCER)) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next(s.stages)) {
+                const int st = ring.s;
+                if (!wait_bar(&sm.empty[st], ring.parity ^ 1, abort, ROLE_PRODUCER)) {
                     ok = false;
                     break;
                 }
@@ -296,26 +331,30 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (leader)
         if (leader) {
-            int it = 0, tc = 0;
+            int tc = 0;
+            Ring ring;
             bool ok = true;
+            // descriptors of stage 0; a stage further is sbytes / 16 more in the address field
+            const uint64_t w_desc0 = desc_kmajor_sw128(smem_u32(stages));
+            const uint64_t a_desc0 = desc_kmajor_sw128(smem_u32(stages) + BW * BKB);
             for (int t = cid; t < tiles && ok; t += nclusters, ++tc) {
                 const Tile tl = decode(sm, s, t, nblk, TILE_N);
                 const uint32_t idesc = PAIR ? idesc_i8(TILE_N, (tl.rows + 31) / 32 * 32)
                                             : idesc_i8(TILE_N, (tl.rows + 15) / 16 * 16);
                 const int buf = tc % bufs;
                 const uint32_t acc = tmem + buf * acc_stride;
-                if (!warp_wait(&sm.acc_empty[buf], ((tc / bufs) & 1) ^ 1, abort, ROLE_MMA)) break;
+                if (!wait_bar(&sm.acc_empty[buf], ((tc / bufs) & 1) ^ 1, abort, ROLE_MMA)) break;
                 tc_fence_after();
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % s.stages;
-                    if (!warp_wait(&sm.full[st], (it / s.stages) & 1, abort, ROLE_MMA)) { ok = false; break; }
+                for (int kb = kb0; kb < kb1; ++kb, ring.next(s.stages)) {
+                    const int st = ring.s;
+                    if (!wait_bar(&sm.full[st], ring.parity, abort, ROLE_MMA)) { ok = false; break; }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t w0 = smem_u32(stages + (size_t)st * sbytes), a0 = w0 + BW * BKB;
+                        const uint32_t step = (uint32_t)(st * (sbytes >> 4));
 #pragma unroll
                         for (int ks = 0; ks < KSTEPS; ++ks)
-                            mma_i8<PAIR>(acc, desc_kmajor_sw128(w0 + ks * 32),
-                                         desc_kmajor_sw128(a0 + ks * 32), idesc, kb != kb0 || ks != 0);
+                            mma_i8<PAIR>(acc, w_desc0 + (step + ks * 2), a_desc0 + (step + ks * 2),
+                                         idesc, kb != kb0 || ks != 0);
                         if constexpr (PAIR) mma_commit_pair(&sm.empty[st], 0x3);
                         else mma_commit(&sm.empty[st]);
                     }
@@ -353,7 +392,7 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             const bool nok = n < s.N;
             const float sw = nok ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
             const int buf = tc % bufs;
-            if (!warp_wait(&sm.acc_full[buf], (tc / bufs) & 1, abort, ROLE_EPI)) break;
+            if (!wait_bar(&sm.acc_full[buf], (tc / bufs) & 1, abort, ROLE_EPI)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
             for (int c = half * 32; c < tl.rows; c += 64) {
@@ -389,12 +428,12 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             stages + (reduce_aliased(s.bt, s.split) ? 0 : (size_t)s.stages * sbytes));
         if (reduce_aliased(s.bt, s.split)) {
             __syncwarp();
-            if (warp >= FIRST_EPI_WARP) warp_wait(&sm.acc_full[0], 0, abort, ROLE_EPI);
+            if (warp >= FIRST_EPI_WARP) wait_bar(&sm.acc_full[0], 0, abort, ROLE_EPI);
             cluster_sync();  // every CTA's MMAs have read their stages
         }
         if (warp >= FIRST_EPI_WARP) {
             const int q = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
-            if (warp_wait(&sm.acc_full[0], 0, abort, ROLE_EPI)) {
+            if (wait_bar(&sm.acc_full[0], 0, abort, ROLE_EPI)) {
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
                 for (int c = half * 32; c < tl.rows; c += 64) {
