@@ -8,19 +8,28 @@
 // the result is rounded once to BF16.
 //
 // The weights are the MMA's M side (channels in TMEM lanes) and the tokens its N side
-// (columns), whatever their number: a tile is 128 channels per CTA by up to `bt`
-// tokens, and the last tile of a group of rows runs the MMA only as wide as its
-// tokens need (N in steps of 16, or of 32 on a pair of SMs).  So a ragged expert or a
-// single token costs no MMA rows of padding, and one code path serves them all.
-//   * int8_kernel<true>: pairs of SMs (tcgen05.mma.cta_group::2.kind::i8, M = 256):
-//     each CTA loads its own 128 channels and half of the tile's tokens.
-//   * int8_kernel<false>: single SMs (M = 128).  With S > 1 a cluster of S CTAs works
-//     on one tile, each on its own range of K; the INT32 partial sums meet in the
-//     owners' shared memory (distributed shared memory, no workspace), every CTA
-//     finishing its share of the tile's tokens.  Integer sums do not depend on order.
-// Warp 0 loads (TMA, 128-byte swizzle), warp 1 issues the MMAs, eight warps apply the
-// scales and store.  With S == 1 the accumulator is double-buffered and the CTAs are
+// (columns), whatever their number: a tile is 256 channels by up to `bt` tokens on a pair
+// of SMs (tcgen05.mma.cta_group::2.kind::i8, M = 256), and the last tile of a group of
+// rows runs the MMA only as wide as its tokens need (N in steps of 32).  So a ragged
+// expert or a single token costs no MMA rows of padding, and one code path serves all.
+//   * Each CTA of the pair loads its own 128 channels and half of the tile's tokens.
+//   * With few tiles a cluster of `split` pairs works on one tile, each pair on its own
+//     range of K; the INT32 partial sums meet in the owners' shared memory (distributed
+//     shared memory, no workspace), every pair finishing its share of the tile's tokens.
+//     Integer sums do not depend on order.
+// Warp 0 loads (TMA, 128-byte swizzle), warp 1 of the leader issues the MMAs, eight warps
+// apply the scales and store.  The accumulator is double-buffered and the clusters are
 // persistent, so a tile's epilogue runs under the next tile's MMAs.
+//
+// What bounds it (B200, zeros where power is not the question): an SM's shared memory
+// takes one 128-byte row a clock, for the TMA writes and the MMA's operand reads alike.  A
+// 128-byte step of K of a full tile costs 256 clocks for the channels (written, read) and
+// bt for the tokens, against 2 bt clocks of MMA: tiles of 256 tokens are the smallest that
+// the MMA bounds.  Measured per step: 156 ns at 64 tokens, 201 at 128, 322 at 256 with
+// every SM busy.  Large products are bound by power: 4096 x 5376 x 14336 takes 163 us on
+// zeros and 199 us on random codes.  Small ones by the weights' bytes (6.2 TB/s reached).
+// Single SMs instead of pairs (M = 128) took 31 us for 333 tokens where pairs take 27, and
+// 78 us for 32 tokens over 8 experts where pairs take 75.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -38,12 +47,15 @@ using w4a4::ROLE_MMA;
 using w4a4::ROLE_PRODUCER;
 
 constexpr int MAX_EXPERTS = grouped_pair::MAX_EXPERTS;
+constexpr int CTAS = 2;          // a pair of SMs per tile and part of K
 constexpr int BW = 128;          // weight rows (channels) per CTA
-constexpr int BKB = 128;         // bytes (= codes) of K per stage row: one swizzle row
+constexpr int TILE_N = CTAS * BW;
+constexpr int BKB = 128;         // bytes (= codes) of K per chunk: one swizzle row
 constexpr int KSTEPS = BKB / 32; // K = 32 per kind::i8 MMA
 constexpr int MAX_BT = 256;      // token columns of a tile
 constexpr int MAX_STAGES = 12;
-constexpr int MAX_SPLIT = 8;     // CTAs of a split tile (portable cluster size)
+constexpr int MAX_CHUNKS = 2;
+constexpr int MAX_SPLIT = 4;     // pairs of a split tile (8 CTAs: the portable cluster size)
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int FIRST_EPI_WARP = 2;
 constexpr int NUM_THREADS = 32 * (FIRST_EPI_WARP + NUM_EPI_WARPS);
@@ -51,8 +63,9 @@ constexpr int MAX_K = 131056;    // 128 * 128 * K < 2^31
 
 struct Shape {
     int M, N, K, E;
-    int bt;      // token columns of a full tile (a multiple of 16; of 32 on pairs)
-    int split;   // CTAs per tile over K (1 on pairs)
+    int bt;      // token columns of a full tile (a multiple of 32)
+    int split;   // pairs per tile over K
+    int chunks;  // 128-byte chunks of K per stage (1 or 2)
     int stages;
 };
 
@@ -63,6 +76,8 @@ struct Smem {
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint64_t drain;
+    uint64_t red_full;  // split tiles: every source's partial sums of the tile are here
+    uint64_t red_free;  // split tiles: every owner has read this CTA's partial sums
     uint32_t tmem_base;
     int abort;
     int bad;
@@ -71,47 +86,62 @@ struct Smem {
 };
 constexpr int HEAD_BYTES = (sizeof(Smem) + 1023) / 1024 * 1024;
 
-__host__ __device__ constexpr int acc_cols(int bt) { return (bt + 31) / 32 * 32; }
-__host__ __device__ constexpr int tmem_cols(int bt, int split) {
-    const int need = acc_cols(bt) * (split > 1 ? 1 : 2);
+__host__ __device__ constexpr int tmem_cols(int bt) {  // two accumulators
     int c = 32;
-    while (c < need) c *= 2;
+    while (c < 2 * bt) c *= 2;
     return c;
 }
-__host__ __device__ constexpr int stage_bytes(bool pair, int bt) {
-    return BW * BKB + (pair ? bt / 2 : bt) * BKB;
+__host__ __device__ constexpr int stage_bytes(int bt, int chunks) {
+    return chunks * (BW + bt / CTAS) * BKB;
 }
-// bytes of the partial sums a CTA of a split tile receives, S sources x its columns x 128
+// Split tiles: CTA o of the cluster finishes token columns [o*cw, (o+1)*cw), cw columns
+// of the tile's `rows`, in whole quads.
+__host__ __device__ constexpr int share_cols(int rows, int split) {
+    return ((rows + split - 1) / split + 3) / 4 * 4;
+}
+// bytes of the partial sums such a CTA receives: S sources x its columns x 128 channels
 __host__ __device__ constexpr int reduce_bytes(int bt, int split) {
-    return split > 1 ? split * ((bt + split - 1) / split) * BW * 4 : 0;
+    return split > 1 ? split * share_cols(bt, split) * BW * 4 : 0;
 }
-// a reduce buffer of its own up to this size; a larger one reuses the stages, which
-// costs one more cluster barrier (all of the cluster's MMAs must be over first)
-constexpr int REDUCE_OWN_BYTES = 36 * 1024;
-__host__ __device__ constexpr bool reduce_aliased(int bt, int split) {
-    return reduce_bytes(bt, split) > REDUCE_OWN_BYTES;
-}
-__host__ __device__ constexpr size_t smem_bytes(bool pair, int bt, int split, int stages) {
-    return 1024 + HEAD_BYTES + (size_t)stages * stage_bytes(pair, bt) +
-           (reduce_aliased(bt, split) ? 0 : reduce_bytes(bt, split));
+constexpr int OUT_BYTES = 32 * BW * 2;  // epilogue staging of a chunk of tokens (whole tiles), twice
+// At least the share of an SM's 228 KB that the CTA takes of its 512 TMEM columns: then
+// CTAs that fit an SM together never wait for each other's TMEM.  (Two clusters that each
+// hold the columns the other one waits for would never end.)
+__host__ __device__ constexpr size_t smem_bytes(int bt, int split, int chunks, int stages) {
+    const size_t need = 1024 + HEAD_BYTES + (size_t)stages * stage_bytes(bt, chunks) +
+                        (split > 1 ? reduce_bytes(bt, split) : 2 * OUT_BYTES);
+    const size_t share = (size_t)tmem_cols(bt) * (228 * 1024 / 512);
+    const size_t most = 227 * 1024;
+    return need >= share ? need : share < most ? share : most;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T with signed 8-bit operands and INT32 sums, K = 32.
-template <bool PAIR>
+// TMEM -> registers: 16 lanes x 256 bit, four times (32 columns): the MMA's fragment
+// layout, row lane / 4 (then row lane / 4 + 8), columns 2 (lane % 4) and the next of each 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Four 8 x 8 blocks of 16-bit values (fragment layout), each stored transposed: lane l
+// gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(void* row, const uint32_t (&m)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(smem_u32(row)), "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3]) : "memory");
+}
+
+// The pair's D[tmem] (+)= A[smem] * B[smem]^T with signed 8-bit operands and INT32 sums,
+// K = 32.
 __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate) {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 // Instruction descriptor of kind::i8: S8 x S8 -> S32, K-major, no saturation.
 //   bits 4-5 D format (2 = S32)    bits 7-9 / 10-12 A/B format (1 = signed 8-bit)
@@ -132,15 +162,32 @@ struct Ring {
     }
 };
 
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Arrive on `bar`'s counterpart in CTA `rank`, releasing at cluster scope.
+__device__ __forceinline__ void arrive_release_cluster(uint64_t* bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                 ::"r"(map_to_rank(bar, rank)) : "memory");
+}
+
 // Bounded wait of a whole converged warp (mbar_wait's limit and error record).  Every lane
 // polls, so no shuffle or branch stands between the barrier and the work behind it, and
 // the clock and the abort flag are looked at once every 32 polls: a K-block of one tile of
 // 16 tokens took 0.35 us with a one-lane wait that reads the clock on every poll, 0.21 us
 // with this one.
+// CLUSTER: acquires what other CTAs of the cluster released on the barrier.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int role) {
     uint64_t t0 = 0;
     bool ok = true;
-    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    for (uint32_t n = 1; !(CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++n) {
         if ((n & 31) == 0) {
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
@@ -155,16 +202,19 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, ok);
 }
 
+// Columns of the MMA of a tile of `rows` tokens.
+__device__ __forceinline__ int mma_n(int rows) { return (rows + 31) / 32 * 32; }
+
 struct Tile {
     int e;
     int m0;    // first token row
     int rows;  // tokens of the tile, 1..bt
-    int n0;    // first channel (of the pair's 256, or of the CTA's 128)
+    int n0;    // first channel of the pair's 256
 };
 
 // Tile t of the list that runs over the experts; within an expert, groups of GROUP_M
 // token blocks sweep the channels together, token blocks fastest (they share weights).
-__device__ __forceinline__ Tile decode(const Smem& sm, const Shape& s, int t, int nblk, int tile_n) {
+__device__ __forceinline__ Tile decode(const Smem& sm, const Shape& s, int t, int nblk) {
     int lo = 0, hi = s.E;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -176,7 +226,7 @@ __device__ __forceinline__ Tile decode(const Smem& sm, const Shape& s, int t, in
     w4a4_pair::tile_coords(t - sm.tb_start[lo] * nblk, sm.tb_start[lo + 1] - sm.tb_start[lo], nblk, mb, nb);
     tl.m0 = sm.row_start[lo] + mb * s.bt;
     tl.rows = min(s.bt, sm.row_start[lo + 1] - tl.m0);
-    tl.n0 = nb * tile_n;
+    tl.n0 = nb * TILE_N;
     return tl;
 }
 
@@ -218,38 +268,49 @@ __device__ __forceinline__ void plan_rows(Smem& sm, const Shape& s, const int32_
     }
 }
 
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ uint32_t map_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+// 16 bytes into the shared memory of a CTA of the cluster, counted on a barrier there
+// (both addresses shared::cluster): the data is visible to whoever waits on the barrier,
+// without a fence on either side.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, uint32_t a, uint32_t b,
+                                            uint32_t c, uint32_t d) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];"
+        ::"r"(addr), "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <bool PAIR>
-__global__ void __launch_bounds__(NUM_THREADS, PAIR ? 1 : 2)
+template <int CHUNKS>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
 int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 128 B x 128 rows
-            const __grid_constant__ CUtensorMap tmA,  // A codes [M][K], box 128 B x bt (pair: bt/2) rows
+            const __grid_constant__ CUtensorMap tmA,  // A codes [M][K], box 128 B x bt/2 rows
             const float* __restrict__ sA, const float* __restrict__ sW,
             const int32_t* __restrict__ offsets,      // device int32 [E+1], or null (E == 1: all M rows)
             __nv_bfloat16* __restrict__ Y, const __grid_constant__ Shape s) {
-    constexpr int CTAS = PAIR ? 2 : 1;
-    constexpr int TILE_N = BW * CTAS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     Smem& sm = *reinterpret_cast<Smem*>(base);
     uint8_t* const stages = base + HEAD_BYTES;
-    const int sbytes = stage_bytes(PAIR, s.bt);
+    const int tokbytes = s.bt / CTAS * BKB;            // this CTA's tokens in one chunk
+    const int sbytes = CHUNKS * (BW * BKB + tokbytes);  // a stage: CHUNKS of W, then of A
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool clustered = PAIR || s.split > 1;
-    const uint32_t rank = clustered ? cluster_ctarank() : 0;
-    const bool leader = !PAIR || rank == 0;
-    const int per = PAIR ? 2 : s.split;  // CTAs of a cluster
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t prank = rank % CTAS, lead = rank - prank;  // rank in its pair, the pair's leader
+    const bool leader = prank == 0;
+    const int part = (int)(rank / CTAS);  // this pair's part of K
+    const int per = CTAS * s.split;       // CTAs of a cluster
     const int cid = blockIdx.x / per, nclusters = gridDim.x / per;
     const int nblk = (s.N + TILE_N - 1) / TILE_N;
-    const int nk = (s.K + BKB - 1) / BKB;
-    // this CTA's K-blocks (all of them unless the tile is split)
-    const int kb0 = PAIR ? 0 : (int)((long long)nk * rank / s.split);
-    const int kb1 = PAIR ? nk : (int)((long long)nk * (rank + 1) / s.split);
-    const int bufs = s.split > 1 ? 1 : 2;
-    const uint32_t acc_stride = (uint32_t)acc_cols(s.bt);
+    const int nk = (s.K + CHUNKS * BKB - 1) / (CHUNKS * BKB);
+    // this pair's K-blocks (all of them unless the tile is split); a chunk past K is all
+    // zeros, as every byte that a box reads out of range
+    const int kb0 = (int)((long long)nk * part / s.split);
+    const int kb1 = (int)((long long)nk * (part + 1) / s.split);
+    const uint32_t acc_stride = (uint32_t)s.bt;
     volatile int* abort = &sm.abort;
 
     if (threadIdx.x == 0) {
@@ -262,6 +323,8 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             mbar_init(&sm.acc_empty[i], CTAS * NUM_EPI_WARPS);
         }
         mbar_init(&sm.drain, 1);
+        mbar_init(&sm.red_full, 1);
+        mbar_init(&sm.red_free, s.split * NUM_EPI_WARPS);
         sm.abort = 0;
         sm.bad = 0;
         fence_mbarrier_init();
@@ -269,20 +332,18 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         tma_prefetch_desc(&tmA);
     }
     if (warp == 1) {
-        if constexpr (PAIR) {
-            tmem_alloc_pair(&sm.tmem_base, tmem_cols(s.bt, s.split));
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(&sm.tmem_base, tmem_cols(s.bt, s.split));
-            tmem_relinquish();
-        }
+        tmem_alloc_pair(&sm.tmem_base, tmem_cols(s.bt));
+        tmem_relinquish_pair();
     }
     __syncthreads();
-    // the set-up above overlaps the kernel before this one; its output is read only from here
+    // The kernel behind this one may start its own set-up now: not earlier, so that its
+    // tensor-memory allocation cannot come before this CTA's.
+    grid_dependents_launch();
+    // The set-up above overlaps the kernel before this one; its output is read only from here.
     grid_dependency_wait();
     if (warp == FIRST_EPI_WARP) plan_rows(sm, s, offsets);
     tc_fence_before();
-    if (clustered) cluster_sync(); else __syncthreads();
+    cluster_sync();  // every CTA's barriers exist before any remote arrive
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     const int tiles = sm.bad ? 0 : sm.tb_start[s.E] * nblk;
@@ -293,10 +354,10 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         Ring ring;
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += nclusters) {
-            const Tile tl = decode(sm, s, t, nblk, TILE_N);
-            const int wrow = tl.e * s.N + tl.n0 + (PAIR ? (int)rank * BW : 0);
+            const Tile tl = decode(sm, s, t, nblk);
+            const int wrow = tl.e * s.N + tl.n0 + (int)prank * BW;
             // a pair's MMA takes the first half of its columns from CTA 0, the rest from CTA 1
-            const int arow = tl.m0 + (PAIR ? (int)rank * ((tl.rows + 31) / 32 * 16) : 0);
+            const int arow = tl.m0 + (int)prank * (mma_n(tl.rows) / 2);
             for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next(s.stages)) {
                 const int st = ring.s;
                 if (!wait_bar(&sm.empty[st], ring.parity ^ 1, abort, ROLE_PRODUCER)) {
@@ -306,13 +367,13 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 if (elect_one()) {
                     uint8_t* w = stages + (size_t)st * sbytes;
                     if (leader) mbar_arrive_expect_tx(&sm.full[st], CTAS * sbytes);
-                    if constexpr (PAIR) {
-                        const uint32_t full0 = map_to_rank(&sm.full[st], 0);
-                        tma_load_2d_pair(w, &tmW, full0, kb * BKB, wrow);
-                        tma_load_2d_pair(w + BW * BKB, &tmA, full0, kb * BKB, arow);
-                    } else {
-                        tma_load_2d(w, &tmW, &sm.full[st], kb * BKB, wrow);
-                        tma_load_2d(w + BW * BKB, &tmA, &sm.full[st], kb * BKB, arow);
+                    uint8_t* a = w + CHUNKS * BW * BKB;
+                    const uint32_t full0 = map_to_rank(&sm.full[st], lead);
+#pragma unroll
+                    for (int c = 0; c < CHUNKS; ++c) {
+                        const int x = (kb * CHUNKS + c) * BKB;
+                        tma_load_2d_pair(w + c * BW * BKB, &tmW, full0, x, wrow);
+                        tma_load_2d_pair(a + c * tokbytes, &tmA, full0, x, arow);
                     }
                 }
                 __syncwarp();
@@ -336,14 +397,13 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             bool ok = true;
             // descriptors of stage 0; a stage further is sbytes / 16 more in the address field
             const uint64_t w_desc0 = desc_kmajor_sw128(smem_u32(stages));
-            const uint64_t a_desc0 = desc_kmajor_sw128(smem_u32(stages) + BW * BKB);
+            const uint64_t a_desc0 = desc_kmajor_sw128(smem_u32(stages) + CHUNKS * BW * BKB);
             for (int t = cid; t < tiles && ok; t += nclusters, ++tc) {
-                const Tile tl = decode(sm, s, t, nblk, TILE_N);
-                const uint32_t idesc = PAIR ? idesc_i8(TILE_N, (tl.rows + 31) / 32 * 32)
-                                            : idesc_i8(TILE_N, (tl.rows + 15) / 16 * 16);
-                const int buf = tc % bufs;
+                const Tile tl = decode(sm, s, t, nblk);
+                const uint32_t idesc = idesc_i8(TILE_N, mma_n(tl.rows));
+                const int buf = tc & 1;
                 const uint32_t acc = tmem + buf * acc_stride;
-                if (!wait_bar(&sm.acc_empty[buf], ((tc / bufs) & 1) ^ 1, abort, ROLE_MMA)) break;
+                if (!wait_bar(&sm.acc_empty[buf], ((tc >> 1) & 1) ^ 1, abort, ROLE_MMA)) break;
                 tc_fence_after();
                 for (int kb = kb0; kb < kb1; ++kb, ring.next(s.stages)) {
                     const int st = ring.s;
@@ -352,24 +412,22 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                     if (elect_one()) {
                         const uint32_t step = (uint32_t)(st * (sbytes >> 4));
 #pragma unroll
-                        for (int ks = 0; ks < KSTEPS; ++ks)
-                            mma_i8<PAIR>(acc, w_desc0 + (step + ks * 2), a_desc0 + (step + ks * 2),
-                                         idesc, kb != kb0 || ks != 0);
-                        if constexpr (PAIR) mma_commit_pair(&sm.empty[st], 0x3);
-                        else mma_commit(&sm.empty[st]);
+                        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+                            for (int ks = 0; ks < KSTEPS; ++ks)
+                                mma_i8(acc, w_desc0 + (step + c * (BW * BKB / 16) + ks * 2),
+                                             a_desc0 + (step + c * (tokbytes >> 4) + ks * 2), idesc,
+                                             kb != kb0 || c != 0 || ks != 0);
+                        mma_commit_pair(&sm.empty[st], 0x3 << lead);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (elect_one()) {
-                    if constexpr (PAIR) mma_commit_pair(&sm.acc_full[buf], 0x3);
-                    else mma_commit(&sm.acc_full[buf]);
-                }
+                if (elect_one()) mma_commit_pair(&sm.acc_full[buf], 0x3 << lead);
                 __syncwarp();
             }
             if (elect_one()) {
-                if constexpr (PAIR) mma_commit_pair(&sm.drain, 0x1);
-                else mma_commit(&sm.drain);
+                mma_commit_pair(&sm.drain, 0x1 << lead);
                 const uint64_t t0 = globaltimer_ns();
                 while (!mbar_try_wait(&sm.drain, 0)) {
                     if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -382,103 +440,154 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         }
     } else if (s.split == 1) {
         // ------------------------------------------------------------ epilogue, whole tiles
-        // lane = channel; the warp's half of the 32-token chunks.  One token's 32 channels
-        // leave as one 64-byte store.
+        // Four warps (one per 32 channels) take each second chunk of 32 tokens, through a
+        // staging buffer of 32 tokens x 128 channels: the accumulator comes in the MMA
+        // fragment layout, is stored transposed (stmatrix) and leaves as whole 256-byte
+        // runs of a token's channels.  (Two-byte stores straight from the registers, 64
+        // bytes of one token per warp, took 6 us for 256 tokens.)
         const int q = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
+        uint8_t* const out = stages + (size_t)s.stages * sbytes + half * OUT_BYTES;
+        const int g = lane >> 2, p2 = (lane & 3) * 2;  // fragment row, first of its two columns
+        const bool wide = s.N % 8 == 0;                // 16-byte stores stay in a row
         int tc = 0;
         for (int t = cid; t < tiles; t += nclusters, ++tc) {
-            const Tile tl = decode(sm, s, t, nblk, TILE_N);
-            const int n = tl.n0 + (PAIR ? (int)rank * BW : 0) + 32 * q + lane;
-            const bool nok = n < s.N;
-            const float sw = nok ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
-            const int buf = tc % bufs;
-            if (!wait_bar(&sm.acc_full[buf], (tc / bufs) & 1, abort, ROLE_EPI)) break;
+            const Tile tl = decode(sm, s, t, nblk);
+            const int n0 = tl.n0 + (int)prank * BW;
+            float sw[4];  // channels g, g + 8, g + 16, g + 24 of the warp's 32
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = n0 + 32 * q + 8 * i + g;
+                sw[i] = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
+            }
+            const int buf = tc & 1;
+            if (!wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
             for (int c = half * 32; c < tl.rows; c += 64) {
-                const float sa = c + lane < tl.rows ? __ldg(sA + tl.m0 + c + lane) : 0.f;
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(acc + c, r);
+                uint32_t r[32];  // [channels 0-15, 16-31][8 tokens][row g, row g + 8][2 tokens]
+                tmem_ld_16x256b_x4(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                tmem_ld_16x256b_x4(acc + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                float sa[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = c + 8 * (i >> 1) + p2 + (i & 1);
+                    sa[i] = j < tl.rows ? __ldg(sA + tl.m0 + j) : 0.f;
+                }
                 tmem_ld_wait();
                 reg_fence(r);
-                __nv_bfloat16* y = Y + (size_t)(tl.m0 + c) * s.N + n;
-                const int cnt = min(32, tl.rows - c);
+                named_bar_sync(1 + half, 128);  // the buffer's last chunk has left
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float f = sw * __shfl_sync(0xffffffffu, sa, j);
-                    if (j < cnt && nok) y[(size_t)j * s.N] = __float2bfloat16_rn((float)(int)r[j] * f);
+                for (int i = 0; i < 4; ++i) {  // 8 tokens
+                    uint32_t m[4];             // 8 x 8 blocks of channels 0, 8, 16, 24
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = (k >> 1) * 16 + i * 4 + (k & 1) * 2;
+                        __nv_bfloat162 h = __floats2bfloat162_rn((float)(int)r[at] * (sw[k] * sa[2 * i]),
+                                                                 (float)(int)r[at + 1] * (sw[k] * sa[2 * i + 1]));
+                        m[k] = *reinterpret_cast<uint32_t*>(&h);
+                    }
+                    // lane l gives the address of row l & 7 (a token) of block l >> 3
+                    const int tok = 8 * i + (lane & 7), blk = 4 * q + (lane >> 3);
+                    stmatrix_x4_trans(out + tok * 256 + ((blk ^ (tok & 7)) << 4), m);
+                }
+                named_bar_sync(1 + half, 128);
+                const int cnt = min(32, tl.rows - c);
+                const int n = n0 + (lane & 15) * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = q * 8 + i * 2 + (lane >> 4);
+                    const uint4 v = *reinterpret_cast<const uint4*>(
+                        out + tok * 256 + ((((lane & 15)) ^ (tok & 7)) << 4));
+                    if (tok < cnt) {
+                        uint16_t* y = reinterpret_cast<uint16_t*>(Y) + (size_t)(tl.m0 + c + tok) * s.N + n;
+                        if (wide) {
+                            if (n < s.N) *reinterpret_cast<uint4*>(y) = v;
+                        } else {
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (n + k < s.N) y[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+                        }
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_remote(&sm.acc_empty[buf], 0);
-                else mbar_arrive(&sm.acc_empty[buf]);
-            }
+            if (lane == 0) mbar_arrive_remote(&sm.acc_empty[buf], lead);
         }
-    }
-
-    if (!PAIR && s.split > 1 && cid < tiles) {
-        // ------------------------------------------------------------ split tile: join the K ranges
-        // CTA `o` of the cluster finishes token columns [o*cw, (o+1)*cw); each CTA leaves
-        // its INT32 partial sums of those columns in o's buffer [source][column][128].
-        const Tile tl = decode(sm, s, cid, nblk, TILE_N);
-        const int cw = (tl.rows + s.split - 1) / s.split;
-        int32_t* red = reinterpret_cast<int32_t*>(
-            stages + (reduce_aliased(s.bt, s.split) ? 0 : (size_t)s.stages * sbytes));
-        if (reduce_aliased(s.bt, s.split)) {
-            __syncwarp();
-            if (warp >= FIRST_EPI_WARP) wait_bar(&sm.acc_full[0], 0, abort, ROLE_EPI);
-            cluster_sync();  // every CTA's MMAs have read their stages
-        }
-        if (warp >= FIRST_EPI_WARP) {
-            const int q = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
-            if (wait_bar(&sm.acc_full[0], 0, abort, ROLE_EPI)) {
-                tc_fence_after();
-                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
-                for (int c = half * 32; c < tl.rows; c += 64) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(acc + c, r);
-                    tmem_ld_wait();
-                    reg_fence(r);
+    } else {
+        // ------------------------------------------------------------ epilogue, split tiles
+        // Each CTA sends its INT32 partial sums to the columns' owners, as [source][column
+        // quad][channel] int4; an owner adds its columns' sums and stores them.
+        const int q = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
+        const int tid = threadIdx.x - 32 * FIRST_EPI_WARP, ch = tid & (BW - 1);
+        uint8_t* const red = stages + (size_t)s.stages * sbytes;
+        int tc = 0;
+        for (int t = cid; t < tiles; t += nclusters, ++tc) {
+            const Tile tl = decode(sm, s, t, nblk);
+            const int cw = share_cols(tl.rows, s.split), quads = cw / 4;
+            const int my_cols = max(0, min(cw, tl.rows - part * cw));
+            const int n = tl.n0 + (int)prank * BW + ch;
+            const float sw = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
+            if (tid == 0) mbar_arrive_expect_tx(&sm.red_full, s.split * ((my_cols + 3) / 4) * BW * 16);
+            const int buf = tc & 1;
+            if (!wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI)) break;
+            // the owners have read this CTA's sums of the tile before
+            if (tc > 0 && !wait_bar<true>(&sm.red_free, (tc - 1) & 1, abort, ROLE_EPI)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
+            const uint32_t src = smem_u32(red) + (uint32_t)(part * quads * BW + 32 * q + lane) * 16;
+            for (int c = half * 32; c < tl.rows; c += 64) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(acc + c, r);
+                tmem_ld_wait();
+                reg_fence(r);
+                int o = c / cw, quad = (c - o * cw) / 4;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int col = c + j, o = col / cw;
-                        if (col < tl.rows)
-                            st_cluster_u32(map_to_rank(red + ((int)rank * cw + col - o * cw) * BW + 32 * q + lane,
-                                                       (uint32_t)o),
-                                           r[j]);
+                for (int j = 0; j < 32; j += 4) {
+                    if (c + j < tl.rows) {
+                        const uint32_t to = (uint32_t)o * CTAS + prank;
+                        st_async_v4(map_addr(src + (uint32_t)(quad * BW * 16), to),
+                                    map_to_rank(&sm.red_full, to), r[j], r[j + 1], r[j + 2], r[j + 3]);
+                    }
+                    if (++quad == quads) {
+                        quad = 0;
+                        ++o;
                     }
                 }
-                tc_fence_before();
             }
-        }
-        __syncwarp();
-        cluster_sync();  // release/acquire: the partial sums are in place
-        if (warp >= FIRST_EPI_WARP && !*abort) {
-            const int tid = threadIdx.x - 32 * FIRST_EPI_WARP;
-            const int n = tl.n0 + (tid & (BW - 1));
-            const int c0 = (int)rank * cw, cnt = min(cw, tl.rows - c0);
-            if (n < s.N) {
-                const float sw = __ldg(sW + (size_t)tl.e * s.N + n);
-                for (int c = tid / BW; c < cnt; c += NUM_EPI_WARPS * 32 / BW) {
-                    int32_t v = 0;
-                    for (int i = 0; i < s.split; ++i) v += red[(i * cw + c) * BW + (tid & (BW - 1))];
-                    const int m = tl.m0 + c0 + c;
-                    Y[(size_t)m * s.N + n] = __float2bfloat16_rn((float)v * (sw * __ldg(sA + m)));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(&sm.acc_empty[buf], lead);
+            if (!wait_bar<true>(&sm.red_full, tc & 1, abort, ROLE_EPI)) break;
+            for (int c = tid / BW; c * 4 < my_cols; c += NUM_EPI_WARPS * 32 / BW) {
+                int4 v = make_int4(0, 0, 0, 0);
+                for (int i = 0; i < s.split; ++i) {
+                    const int4 p = *reinterpret_cast<const int4*>(red + ((i * quads + c) * BW + ch) * 16);
+                    v.x += p.x;
+                    v.y += p.y;
+                    v.z += p.z;
+                    v.w += p.w;
                 }
+                const int sum[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c * 4 + j < my_cols && n < s.N) {
+                        const int m = tl.m0 + part * cw + c * 4 + j;
+                        Y[(size_t)m * s.N + n] = __float2bfloat16_rn((float)sum[j] * (sw * __ldg(sA + m)));
+                    }
             }
+            __syncwarp();
+            if (t + nclusters < tiles && lane < s.split)
+                arrive_release_cluster(&sm.red_free, (uint32_t)lane * CTAS + prank);
         }
     }
 
-    // No CTA of a pair leaves (or frees TMEM) while the other may still use it.
+    // No CTA of a cluster leaves (or frees a pair's TMEM) while another may still use it.
     tc_fence_before();
-    if constexpr (PAIR) cluster_sync(); else __syncthreads();
+    cluster_sync();
     tc_fence_after();
-    if (warp == 1) {
-        if constexpr (PAIR) tmem_dealloc_pair(tmem, tmem_cols(s.bt, s.split));
-        else tmem_dealloc(tmem, tmem_cols(s.bt, s.split));
-    }
+    if (warp == 1) tmem_dealloc_pair(tmem, tmem_cols(s.bt));
 }
 
 }  // namespace int8

@@ -93,6 +93,7 @@ int8_quantize_kernel(const uint4* __restrict__ X, int rows, int K, int8_t* __res
     const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const int row = blockIdx.x * RPB + sub;
     const int nv = K / 8;
+    grid_dependents_launch();  // the kernel behind may set itself up; it waits for this one's end
     grid_dependency_wait();
     const uint4* x = X + (size_t)row * nv;
     uint4 v[VPT ? VPT : 1];

@@ -48,6 +48,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
     const unsigned FULL = 0xffffffffu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * WARPS + warp;
+    grid_dependents_launch();  // the kernel behind may set itself up; it waits for this one's end
     grid_dependency_wait();
     if (t >= p.T) return;
     const double NEG = -__longlong_as_double(0x7FF0000000000000ll);

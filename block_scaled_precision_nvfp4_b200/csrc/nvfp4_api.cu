@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1342,46 +1343,110 @@ nvfp4_status gemm_nvfp4_w4a4_grouped(const uint8_t* A, const uint8_t* sA, float 
 
 // ------------------------------------------------------------------------- INT8
 namespace {
-// How an INT8 product runs: on pairs or single SMs, the tile's token columns, the CTAs
-// that share a tile's K range, the stages and the grid.
+// How an INT8 product runs: the tile's token columns, the pairs that share a tile's K
+// range, the stages and the grid.
 struct Int8Plan {
-    bool pair = false;
     nvfp4::int8::Shape shape{};
-    long long tiles = 0;  // an upper bound (the token blocks are known on the device only)
+    long long tiles = 0;  // an upper bound (grouped token blocks are known on the device only)
     int grid = 0;
     size_t smem = 0;
 };
 
 constexpr size_t kInt8SmemMax = 227 * 1024;
-constexpr size_t kInt8SmemTwo = 113 * 1024;  // two CTAs fit one SM
 
-Int8Plan int8_plan(int M, int N, int K, int E, int num_sms) {
+// Clusters of each size that the device runs at once (a cluster stays within one group of
+// SMs, so these are fewer than the SMs divided by its CTAs); 1 at least.
+struct Int8Slots {
+    int clusters[nvfp4::int8::MAX_SPLIT + 1] = {};
+};
+std::mutex g_int8_slots_mu;
+Int8Slots g_int8_slots[64];
+
+nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
     namespace i8 = nvfp4::int8;
-    Int8Plan p;
-    const int nk = (K + i8::BKB - 1) / i8::BKB;
-    const int avg = (int)(((long long)M + E - 1) / E);  // rows of an expert, on average
-    auto blocks = [&](int bt) { return std::min<long long>(M, M / bt + std::min(E, M)); };
-    int bt, split = 1;
-    p.pair = avg > 256;
-    if (p.pair) {
-        bt = i8::MAX_BT;
-        p.tiles = blocks(bt) * ((N + 2 * i8::BW - 1) / (2 * i8::BW));
-    } else {
-        const long long want = E == 1 ? M : 2ll * avg;
-        bt = (int)std::min<long long>((want + 15) / 16 * 16, i8::MAX_BT);
-        p.tiles = blocks(bt) * ((N + i8::BW - 1) / i8::BW);
-        const int slots = bt <= 128 ? 2 * num_sms : num_sms;
-        while (split < i8::MAX_SPLIT && p.tiles * split * 2 <= slots && split * 8 <= nk) split *= 2;
+    std::lock_guard<std::mutex> lk(g_int8_slots_mu);
+    Int8Slots& s = g_int8_slots[dev];
+    if (s.clusters[1] == 0) {
+        nvfp4_status st = set_smem(i8::int8_kernel<2>, kInt8SmemMax, info, "int8_kernel");
+        if (st != NVFP4_OK) return st;
+        for (int sp = i8::MAX_SPLIT; sp >= 1; --sp) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(info.num_sms / (i8::CTAS * sp) * i8::CTAS * sp));
+            cfg.blockDim = dim3(i8::NUM_THREADS);
+            cfg.dynamicSmemBytes = kInt8SmemMax;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)(i8::CTAS * sp);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, i8::int8_kernel<2>, &cfg);
+            if (e != cudaSuccess) return cuda_fail(e, "counting the clusters that run at once");
+            s.clusters[sp] = std::max(1, n);
+        }
     }
-    const size_t budget = !p.pair && split > 1 && bt <= 128 ? kInt8SmemTwo : kInt8SmemMax;
+    out = s;
+    return NVFP4_OK;
+}
+
+// The plan with the least expected time of those that differ in token columns and in the
+// pairs per tile, by the kernel's own measured costs (B200; M x 5376 x 14336):
+//   a 128-byte step of K   100 + 0.87 bt ns, at least 150   (64 tokens 156, 128 201, 256 322)
+//   the weights' bytes     6.2 TB/s
+//   a split tile           0.2 us + 45 ns per token for the exchange of sums
+//                          (64 tokens: 18.3 us on 3 pairs a tile, 21.5 unsplit)
+//   a pair that takes part 8 ns
+// A split is taken only where all of its clusters run at once: with several split tiles
+// per cluster the exchange is not hidden (333 tokens: 43 us on 3 pairs a tile, 27 unsplit).
+Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
+    namespace i8 = nvfp4::int8;
+    const int steps = (K + i8::BKB - 1) / i8::BKB;
+    const long long nblk = (N + i8::TILE_N - 1) / i8::TILE_N;
+    const int live = std::min(E, M);  // experts that can have a row
+    // token blocks of c columns: one group's exactly; of several, at most
+    auto blocks_at_most = [&](int c) -> long long {
+        return E == 1 ? (M + c - 1) / c : std::min<long long>(M, M / c + live);
+    };
+    const double mem_us = ((double)live * N * K + (double)M * K + 2.0 * M * N) / 6.2e6;
+    Int8Plan p;
+    double best = 1e30;
+    int bt = 32, split = 1;
+    for (int c = 32; c <= i8::MAX_BT; c += 32) {
+        // of several groups, half and half: all of one size, or of many sizes, where half a
+        // block of each goes to its ragged end
+        const long long bound = blocks_at_most(c);
+        const int avg = (M + live - 1) / live;
+        const double blocks = E == 1 ? bound
+                                     : 0.5 * ((double)live * ((avg + c - 1) / c) +
+                                              std::max<double>(live, (double)M / c + 0.5 * live));
+        for (int sp = 1; sp <= i8::MAX_SPLIT; ++sp) {
+            if (sp > 1 && (bound * nblk > slots.clusters[sp] || steps < 2 * sp || c > 128)) break;
+            const double per = (steps + sp - 1) / sp * std::max(0.150, 0.100 + 0.00087 * c);
+            const double w = blocks * nblk / slots.clusters[sp];
+            // few waves end with a partly idle one; many even out (experts differ in size)
+            const double waves = E == 1 || w < 2 ? std::ceil(w) : w + 0.5;
+            const double compute = waves * per;
+            const double us = std::max(compute, mem_us) + 0.15 * compute + 0.004 * c +
+                              0.008 * sp * std::min<double>(bound * nblk, slots.clusters[sp]) +
+                              (sp > 1 ? 0.2 + 0.045 * std::min(c, M) : 0.0);
+            if (us < best) {
+                best = us;
+                bt = c;
+                split = sp;
+            }
+        }
+    }
+    p.tiles = blocks_at_most(bt) * nblk;
+    // two 128-byte chunks a stage halve the barriers per byte; wide tiles have the MMAs to
+    // hide them and want the finer stages (192 tokens: 33 us with one chunk, 37 with two)
+    const int chunks = bt <= 128 ? 2 : 1;
     int stages = 2;
-    while (stages < i8::MAX_STAGES && i8::smem_bytes(p.pair, bt, split, stages + 1) <= budget) ++stages;
-    p.shape = {M, N, K, E, bt, split, stages};
-    p.smem = i8::smem_bytes(p.pair, bt, split, stages);
-    const int per = p.pair ? 2 : split;
-    long long clusters = p.tiles;
-    if (split == 1) clusters = std::min<long long>(clusters, num_sms / per);
-    p.grid = (int)std::min<long long>(clusters * per, 1ll << 30);
+    while (stages < i8::MAX_STAGES && i8::smem_bytes(bt, split, chunks, stages + 1) <= kInt8SmemMax) ++stages;
+    p.shape = {M, N, K, E, bt, split, chunks, stages};
+    p.smem = i8::smem_bytes(bt, split, chunks, stages);
+    p.grid = (int)std::min<long long>(p.tiles, slots.clusters[split]) * i8::CTAS * split;
     return p;
 }
 
@@ -1408,15 +1473,17 @@ nvfp4_status launch_int8(const int8_t* A, const float* sA, const int8_t* W, cons
         return fail(NVFP4_ERR_NOPATH, "no INT8 kernel is compiled for sm_%d", info.sm_arch);
     if (M == 0 || N == 0) return ok();
 
-    const Int8Plan p = int8_plan(M, N, K, E, info.num_sms);
-    if (p.tiles > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "M x N too large");
     nvfp4_status st;
+    Int8Slots slots;
+    if ((st = int8_slots(dev, info, slots)) != NVFP4_OK) return st;
+    const Int8Plan p = int8_plan(M, N, K, E, slots);
+    if (p.tiles > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "M x N too large");
     CUtensorMap tmW, tmA;
     if ((st = make_map_u8(&tmW, W, (uint64_t)K, (uint64_t)E * N, i8::BKB, i8::BW)) != NVFP4_OK) return st;
     if ((st = make_map_u8(&tmA, A, (uint64_t)K, (uint64_t)M, i8::BKB,
-                          (uint32_t)(p.pair ? p.shape.bt / 2 : p.shape.bt))) != NVFP4_OK)
+                          (uint32_t)(p.shape.bt / i8::CTAS))) != NVFP4_OK)
         return st;
-    auto kern = p.pair ? i8::int8_kernel<true> : i8::int8_kernel<false>;
+    auto kern = p.shape.chunks == 2 ? i8::int8_kernel<2> : i8::int8_kernel<1>;
     // the attribute's ceiling is the same on every call: calls of other host threads may
     // sit between setting it and launching
     if ((st = set_smem(kern, kInt8SmemMax, info, "int8_kernel")) != NVFP4_OK) return st;
@@ -1430,11 +1497,11 @@ nvfp4_status launch_int8(const int8_t* A, const float* sA, const int8_t* W, cons
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)(p.pair ? 2 : p.shape.split);
+    attr[1].val.clusterDim.x = (unsigned)(i8::CTAS * p.shape.split);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
+    cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmW, tmA, sA, sW, offsets,
                                        reinterpret_cast<__nv_bfloat16*>(Y), p.shape);
     if (e != cudaSuccess) return cuda_fail(e, "launching int8_kernel");
