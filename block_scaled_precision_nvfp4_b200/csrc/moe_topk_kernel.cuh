@@ -12,10 +12,19 @@
 // value; a NaN choice or group score counts as -Inf.  A row without any logit above -Inf
 // has the score 0 for every expert.
 //
-// Choices are compared in 64 bits: without a bias they order like the logits, which are
-// compared instead; with one, neighbouring sums can differ by less than an FP32 step.
+// The ids are those of the 64-bit values (neighbouring choices can differ by less than an
+// FP32 step), at FP32's price: without a bias experts order like their logits, which are
+// compared as they are.  Otherwise the choices are computed in FP32 with a proven error
+// bound; the list of the best is extended until nothing outside it can belong to the first
+// k, and where two neighbours are closer than the bound allows, it is ranked again by
+// 64-bit choices, one list entry per lane.  What that cannot settle (sums of a softmax,
+// groups closer than the bound, more near-ties than lanes) goes through the whole token
+// in 64 bits.  Weights are always 64-bit values of the k chosen scores, rounded once.
 //
-// One warp per token; a group's experts sit on `lpg` neighbouring lanes, V per lane.
+// One warp per token; a group's experts sit on `lpg` neighbouring lanes, V per lane, in
+// ascending order, so the lowest lane and the lowest slot hold the lowest index.  Few
+// bytes, many instructions: 8192 tokens over 256 experts in 8 groups (8.9 MB, 1.4 us of
+// HBM) are bound by the issue slots of the k selection rounds.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -38,19 +47,18 @@ struct Params {
     int renorm;
     float scale;
     int per, lpg;    // experts of a group, lanes of a group
+    int vec;         // every lane's run of logits starts on a 16-byte (BF16: 8-byte) boundary
 };
 
+constexpr float FLT_LARGEST = 3.402823466e38f;
+
+// One token by the formulas in 64 bits, by its whole warp.
 template <int V, typename X>
-__global__ void __launch_bounds__(32 * WARPS)
-moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
-                int32_t* __restrict__ ids, float* __restrict__ weights,
-                const __grid_constant__ Params p) {
+__device__ __noinline__ void topk_exact(const X* __restrict__ logits, const float* __restrict__ bias,
+                                        int32_t* __restrict__ ids, float* __restrict__ weights,
+                                        const Params& p, int t) {
     const unsigned FULL = 0xffffffffu;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * WARPS + warp;
-    grid_dependents_launch();  // the kernel behind may set itself up; it waits for this one's end
-    grid_dependency_wait();
-    if (t >= p.T) return;
+    const int lane = threadIdx.x & 31;
     const double NEG = -__longlong_as_double(0x7FF0000000000000ll);
     const int g = lane / p.lpg, i0 = (lane % p.lpg) * V;
     const int e0 = g * p.per + i0;
@@ -63,7 +71,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         x[v] = NEG;
         if (v < cnt) {
             const float f = (float)logits[(size_t)t * p.E + e0 + v];
-            if (f == f) x[v] = (double)fminf(f, 3.402823466e38f);
+            if (f == f) x[v] = (double)fminf(f, FLT_LARGEST);
         }
         xmax = fmax(xmax, x[v]);
     }
@@ -154,6 +162,238 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         if (p.renorm) w = total > 0.0 ? w / total : 0.0;
         ids[(size_t)t * p.k + lane] = my_id;
         weights[(size_t)t * p.k + lane] = (float)(w * (double)p.scale);
+    }
+}
+
+// Order-preserving key of an FP32 value (never 0: that is left for "no expert").
+__device__ __forceinline__ uint32_t order_key(float f) {
+    const uint32_t b = __float_as_uint(f + 0.0f);  // -0 counts as +0
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// At least twice the error of an FP32 choice whose terms are of size `mag`: two choices
+// further apart order as their real values do.  In units of 2^-24, with __expf off by
+// 2 + 1.173 |x| steps (4 + 2.35 |x| units) and expf by one step:
+//   sigmoid: exp moves s by at most 1.6 (s (1 - s) <= 1/4 and s (1 - s) |x| <= 0.23);
+//     1 + exp adds 1, the fast division 4: 6.6 in all.
+//   softmax: exp is off by 2 + d relative at d = max - x (its argument's rounding), at
+//     most 2.4 of s <= 1 (s d <= 0.37); the sum by 29 (the same, d weighted by the terms
+//     at most ln 256, and 21 additions); the division and the product add 2: 34 in all.
+//   the bias' addition: |c|.
+__device__ __forceinline__ float gap(float mag, bool sigmoid) {
+    return (sigmoid ? 16.0f : 74.0f) * 0x1p-24f + fabsf(mag) * 0x1p-22f;
+}
+
+template <int V, typename X>
+__device__ __forceinline__ void load_logits(const X* __restrict__ row, int e0, int cnt, bool vec,
+                                            float (&x)[V]) {
+    if (vec && cnt == V) {
+        if constexpr (sizeof(X) == 4 && V % 4 == 0) {
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(row + e0 + v));
+                x[v] = f.x, x[v + 1] = f.y, x[v + 2] = f.z, x[v + 3] = f.w;
+            }
+        } else if constexpr (sizeof(X) == 2 && V % 4 == 0) {
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + e0 + v));
+                x[v] = __uint_as_float(u.x << 16), x[v + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+                x[v + 2] = __uint_as_float(u.y << 16), x[v + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = v < cnt ? (float)row[e0 + v] : -INFINITY;
+    }
+    // NaN counts as -Inf (fmaxf drops it), +Inf as the largest finite value
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = fminf(fmaxf(x[v], -INFINITY), FLT_LARGEST);
+}
+
+template <int V, typename X>
+__global__ void __launch_bounds__(32 * WARPS)
+moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
+                int32_t* __restrict__ ids, float* __restrict__ weights,
+                const __grid_constant__ Params p) {
+    const unsigned FULL = 0xffffffffu;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * WARPS + warp;
+    grid_dependents_launch();  // the kernel behind may set itself up; it waits for this one's end
+    grid_dependency_wait();
+    if (t >= p.T) return;
+    const int g = lane / p.lpg, i0 = (lane % p.lpg) * V;
+    const int e0 = g * p.per + i0;
+    const int cnt = g < p.groups ? max(0, min(V, p.per - i0)) : 0;
+    const X* const row = logits + (size_t)t * p.E;
+    const bool group_sum = p.groups > 1 && p.group_top == 2 && p.per > 1;
+
+    float c[V];  // what the experts are ordered by: the choices, or without a bias the logits
+    load_logits<V, X>(row, e0, cnt, p.vec != 0, c);
+    float xmax = 0.f, sum = 0.f;
+    if (!p.sigmoid) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = max(m, order_key(c[v]));
+        xmax = key_value(__reduce_max_sync(FULL, m));
+    }
+    float s[V];  // FP32 scores, where something is ordered or summed by them
+    const bool scores = bias || group_sum || (!p.sigmoid && !p.renorm);
+    if (scores) {
+        if (p.sigmoid) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = __fdividef(1.0f, 1.0f + __expf(-c[v]));
+            // __fdividef gives 0 beyond 2^126, as does the formula to within 2^-126
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[v] = c[v] > -INFINITY ? expf(c[v] - xmax) : 0.f;
+                sum += s[v];
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+            const float inv = sum > 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] *= inv;
+        }
+    }
+    if (bias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float b = v < cnt ? __ldg(bias + e0 + v) : 0.f;
+            c[v] = fmaxf(s[v] + b, -INFINITY);  // a NaN counts as -Inf
+        }
+    }
+
+    bool kept = g < p.groups;
+    if (p.groups > 1) {
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float q = v < cnt ? (group_sum && !bias ? s[v] : c[v]) : -INFINITY;
+            b = fmaxf(b, fminf(a, q));
+            a = fmaxf(a, q);
+        }
+        for (int o = 1; o < p.lpg; o <<= 1) {
+            const float a2 = __shfl_xor_sync(FULL, a, o), b2 = __shfl_xor_sync(FULL, b, o);
+            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+            a = fmaxf(a, a2);
+        }
+        const float gs = fmaxf(group_sum ? a + b : a, -INFINITY);
+        // groups of lower index with an equal score come first
+        int better = 0;
+        for (int h = 0; h < p.groups; ++h) {
+            const float o = __shfl_sync(FULL, gs, h * p.lpg);
+            better += o > gs || (o == gs && h < g);
+        }
+        const bool exists = kept;
+        kept = kept && better < p.top_groups;
+        if ((bias || group_sum) && p.top_groups < p.groups) {
+            // the worst kept group and the best one left out, too close to call?
+            const float lo = key_value(__reduce_min_sync(FULL, kept ? order_key(gs) : 0xFFFFFFFFu));
+            const float hi = key_value(__reduce_max_sync(FULL, exists && !kept ? order_key(gs) : 0u));
+            // the terms of the largest finite sum bound every sum's error (infinite ones are exact)
+            const float mag = key_value(__reduce_max_sync(
+                FULL, order_key(exists && fabsf(gs) < INFINITY ? fabsf(a) + (group_sum ? fabsf(b) : 0.f) : 0.f)));
+            if (lo - hi <= 2.0f * gap(mag, p.sigmoid != 0)) {  // false for two equal infinities
+                topk_exact<V, X>(logits, bias, ids, weights, p, t);
+                return;
+            }
+        }
+    }
+
+    // selection rounds: lane j takes the j-th best; a few more than k while they are too
+    // close to the k-th
+    unsigned left = kept ? (1u << cnt) - 1u : 0u;
+    uint32_t best = 0;  // this lane's best expert left: its key and slot
+    int slot = 0;
+    auto rescan = [&]() {
+        best = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t q = (left >> v & 1u) ? order_key(c[v]) : 0u;
+            if (q > best) {
+                best = q;
+                slot = v;
+            }
+        }
+    };
+    rescan();
+    uint32_t my_key = 0, kth = 0, last = 0;
+    int my_id = 0, n = 0;
+    while (n < 32) {
+        const uint32_t top = __reduce_max_sync(FULL, best);
+        if (top == 0) break;  // no expert left
+        if (n >= p.k) {
+            // the rest is out of reach, or equal to the k-th without rounding (then the
+            // index decides, and the lower ones are in)
+            const float a = key_value(kth);
+            if (!bias || !(a - key_value(top) <= gap(a, p.sigmoid != 0))) break;
+        }
+        const int src = __ffs(__ballot_sync(FULL, best == top)) - 1;
+        const int id = __shfl_sync(FULL, e0 + slot, src);
+        if (lane == n) {
+            my_key = top;
+            my_id = id;
+        }
+        if (lane == src) {
+            left &= ~(1u << slot);
+            rescan();
+        }
+        if (n == p.k - 1) kth = top;
+        last = top;
+        ++n;
+    }
+    bool near = false;
+    if (bias) {
+        const uint32_t next = __shfl_down_sync(FULL, my_key, 1);
+        const float a = key_value(my_key);
+        near = __any_sync(FULL, lane + 1 < n && a - key_value(next) <= gap(a, p.sigmoid != 0));
+        const float k0 = key_value(kth);
+        const bool more = n == 32 && p.k < 32 && k0 - key_value(last) <= gap(k0, p.sigmoid != 0);
+        const bool full = p.k == 32 && __reduce_max_sync(FULL, best) != 0;  // no lane to look further
+        if (more || full || (near && !p.sigmoid)) {
+            topk_exact<V, X>(logits, bias, ids, weights, p, t);
+            return;
+        }
+    }
+
+    // 64-bit scores of the list, one per lane
+    const bool live = lane < n;
+    double x = 0.0, sc = 0.0;
+    if (live) {
+        float f = (float)row[my_id];
+        f = fminf(fmaxf(f, -INFINITY), FLT_LARGEST);
+        x = (double)f;
+        sc = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : f > -INFINITY ? exp(x - (double)xmax) : 0.0;
+    }
+    int rank = lane;
+    if (near) {
+        const double NEG = -__longlong_as_double(0x7FF0000000000000ll);
+        double ch = live ? sc + (double)__ldg(bias + my_id) : NEG;
+        if (!(ch == ch)) ch = NEG;
+        rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const double o = __shfl_sync(FULL, ch, i);
+            const int oi = __shfl_sync(FULL, my_id, i);
+            rank += o > ch || (o == ch && oi < my_id);
+        }
+    }
+    const bool chosen = live && rank < p.k;
+    double w = sc;
+    if (p.renorm) {
+        double total = chosen ? sc : 0.0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(FULL, total, o);
+        w = total > 0.0 ? sc / total : 0.0;
+    } else if (!p.sigmoid) {
+        w = sum > 0.f ? sc / (double)sum : 0.0;
+    }
+    if (chosen) {
+        ids[(size_t)t * p.k + rank] = my_id;
+        weights[(size_t)t * p.k + rank] = (float)(w * (double)p.scale);
     }
 }
 

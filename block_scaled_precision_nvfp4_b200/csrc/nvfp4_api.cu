@@ -1611,9 +1611,10 @@ nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, i
         return fail(NVFP4_ERR_NOPATH, "the router is compiled for sm_100 only (device sm_%d)", info.sm_arch);
     if (T == 0) return ok();
     tk::Params p = {T, E, k, score == NVFP4_SCORE_SIGMOID, groups, top_groups, group_top,
-                    renormalize != 0, scale, per, 32};
+                    renormalize != 0, scale, per, 32, 0};
     while (p.lpg * groups > 32) p.lpg /= 2;  // a power of two of lanes for each group
     const int v = (per + p.lpg - 1) / p.lpg;
+    p.vec = v > 2 && E % 4 == 0 && per % 4 == 0;  // runs of 4 or more
     const dim3 grid((unsigned)((T + tk::WARPS - 1) / tk::WARPS));
     cudaError_t e;
     if (logits_bf16)
