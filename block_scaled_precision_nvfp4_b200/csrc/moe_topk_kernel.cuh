@@ -304,47 +304,56 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         }
     }
 
-    // selection rounds: lane j takes the j-th best; a few more than k while they are too
-    // close to the k-th
-    unsigned left = kept ? (1u << cnt) - 1u : 0u;
-    uint32_t best = 0;  // this lane's best expert left: its key and slot
-    int slot = 0;
-    auto rescan = [&]() {
-        best = 0;
+    // The lane's experts in descending order (a stable network: equal keys keep their
+    // order), then selection rounds: the best head of all lanes leaves its list, and lane j
+    // takes the j-th; a few more than k while they are too close to the k-th.
+    uint32_t key[V];
+    int slot[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const uint32_t q = (left >> v & 1u) ? order_key(c[v]) : 0u;
-            if (q > best) {
-                best = q;
-                slot = v;
-            }
+    for (int v = 0; v < V; ++v) {
+        key[v] = kept && v < cnt ? order_key(c[v]) : 0u;
+        slot[v] = e0 + v;
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < V; ++i)
+#pragma unroll
+        for (int j = V - 1; j > i; --j) {
+            const bool swap = key[j] > key[j - 1];
+            const uint32_t hi = max(key[j], key[j - 1]), lo = min(key[j], key[j - 1]);
+            const int a = swap ? slot[j] : slot[j - 1], b = swap ? slot[j - 1] : slot[j];
+            key[j - 1] = hi, key[j] = lo;
+            slot[j - 1] = a, slot[j] = b;
         }
-    };
-    rescan();
     uint32_t my_key = 0, kth = 0, last = 0;
     int my_id = 0, n = 0;
-    while (n < 32) {
-        const uint32_t top = __reduce_max_sync(FULL, best);
-        if (top == 0) break;  // no expert left
-        if (n >= p.k) {
-            // the rest is out of reach, or equal to the k-th without rounding (then the
-            // index decides, and the lower ones are in)
-            const float a = key_value(kth);
-            if (!bias || !(a - key_value(top) <= gap(a, p.sigmoid != 0))) break;
-        }
-        const int src = __ffs(__ballot_sync(FULL, best == top)) - 1;
-        const int id = __shfl_sync(FULL, e0 + slot, src);
+    auto take = [&](uint32_t top) {
+        const int src = __ffs(__ballot_sync(FULL, key[0] == top)) - 1;
+        const int id = __shfl_sync(FULL, slot[0], src);
         if (lane == n) {
             my_key = top;
             my_id = id;
         }
-        if (lane == src) {
-            left &= ~(1u << slot);
-            rescan();
+        const bool pop = lane == src;
+#pragma unroll
+        for (int v = 0; v + 1 < V; ++v) {
+            key[v] = pop ? key[v + 1] : key[v];
+            slot[v] = pop ? slot[v + 1] : slot[v];
         }
-        if (n == p.k - 1) kth = top;
+        if (pop) key[V - 1] = 0;
         last = top;
         ++n;
+    };
+    while (n < p.k) take(__reduce_max_sync(FULL, key[0]));  // k experts are kept at least
+    kth = last;
+    if (bias) {
+        // experts out of reach of the k-th end the list; so does one equal to it without
+        // rounding (two infinities), where the index has decided already
+        const float a = key_value(kth);
+        while (n < 32) {
+            const uint32_t top = __reduce_max_sync(FULL, key[0]);
+            if (top == 0 || !(a - key_value(top) <= gap(a, p.sigmoid != 0))) break;
+            take(top);
+        }
     }
     bool near = false;
     if (bias) {
@@ -353,7 +362,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         near = __any_sync(FULL, lane + 1 < n && a - key_value(next) <= gap(a, p.sigmoid != 0));
         const float k0 = key_value(kth);
         const bool more = n == 32 && p.k < 32 && k0 - key_value(last) <= gap(k0, p.sigmoid != 0);
-        const bool full = p.k == 32 && __reduce_max_sync(FULL, best) != 0;  // no lane to look further
+        const bool full = p.k == 32 && __reduce_max_sync(FULL, key[0]) != 0;  // no lane to look further
         if (more || full || (near && !p.sigmoid)) {
             topk_exact<V, X>(logits, bias, ids, weights, p, t);
             return;
