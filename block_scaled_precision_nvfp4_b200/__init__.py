@@ -776,15 +776,22 @@ _raw = None
 
 
 def _raw_calls():
-    """(current device index, current raw stream of a device index), as plain calls."""
+    """Three plain calls: the current device index, a device index's current raw stream, and
+    an uninitialised contiguous tensor (size, stride, dtype) on the current device."""
     global _raw
     if _raw is None:
         torch = _torch()
         c = torch._C
         if hasattr(c, "_cuda_getDevice") and hasattr(c, "_cuda_getCurrentRawStream"):
-            _raw = (c._cuda_getDevice, c._cuda_getCurrentRawStream)
+            get = (c._cuda_getDevice, c._cuda_getCurrentRawStream)
         else:
-            _raw = (torch.cuda.current_device, lambda i: torch.cuda.current_stream(i).cuda_stream)
+            get = (torch.cuda.current_device, lambda i: torch.cuda.current_stream(i).cuda_stream)
+        empty = getattr(getattr(getattr(c, "_dynamo", None), "guards", None),
+                        "_empty_strided_cuda", None)
+        if empty is None:
+            def empty(size, stride, dtype):
+                return torch.empty(size, dtype=dtype, device="cuda")
+        _raw = get + (empty,)
     return _raw
 
 
@@ -834,10 +841,15 @@ def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
     psa = _ptr(sA, torch.float32, (M,), "sA", dev)
     pw = _ptr(W, torch.int8, (N, K), "W", dev)
     psw = _ptr(sW, torch.float32, (N,), "sW", dev)
+    _, raw_stream, empty = _raw_calls()
     if out is None:
-        out = A.new_empty((M, N), dtype=torch.bfloat16)
-    py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
-    _err(load_library().gemm_int8_w8a8(pa, psa, pw, psw, py, M, N, K, _raw_calls()[1](dev)))
+        out = empty((M, N), (N, 1), torch.bfloat16)
+        py = out.data_ptr()
+    else:
+        py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
+    st = load_library().gemm_int8_w8a8(pa, psa, pw, psw, py, M, N, K, raw_stream(dev))
+    if st:
+        _err(st)
     return out
 
 
@@ -858,11 +870,15 @@ def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
     pw = _ptr(W, torch.int8, (E, N, K), "W", dev)
     psw = _ptr(sW, torch.float32, (E, N), "sW", dev)
     po = _ptr(offsets, torch.int32, (E + 1,), "offsets", dev)
+    _, raw_stream, empty = _raw_calls()
     if out is None:
-        out = A.new_empty((M, N), dtype=torch.bfloat16)
-    py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
-    _err(load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K,
-                                               _raw_calls()[1](dev)))
+        out = empty((M, N), (N, 1), torch.bfloat16)
+        py = out.data_ptr()
+    else:
+        py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
+    st = load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K, raw_stream(dev))
+    if st:
+        _err(st)
     return out
 
 
@@ -878,16 +894,20 @@ def _int8_quantize(x, dest, k, out, stream):
     n = rows if dest is None else rows * k
     px = _ptr(x, torch.bfloat16, (rows, K), "x", dev)
     pd = None if dest is None else _ptr(dest, torch.int32, (n,), "dest", dev)
+    _, raw_stream, empty = _raw_calls()
     if out is None:
-        out = (x.new_empty((n, K), dtype=torch.int8), x.new_empty((n,), dtype=torch.float32))
-    codes, scales = out
-    pc = _ptr(codes, torch.int8, (n, K), "codes", dev)
-    ps = _ptr(scales, torch.float32, (n,), "scales", dev)
-    lib, st = load_library(), _raw_calls()[1](dev)
-    if dest is None:
-        _err(lib.int8_quantize_bf16(px, rows, K, pc, ps, st))
+        codes, scales = empty((n, K), (K, 1), torch.int8), empty((n,), (1,), torch.float32)
+        pc, ps = codes.data_ptr(), scales.data_ptr()
     else:
-        _err(lib.int8_quantize_bf16_routed(px, rows, K, pd, k, pc, ps, st))
+        codes, scales = out
+        pc = _ptr(codes, torch.int8, (n, K), "codes", dev)
+        ps = _ptr(scales, torch.float32, (n,), "scales", dev)
+    if dest is None:
+        st = load_library().int8_quantize_bf16(px, rows, K, pc, ps, raw_stream(dev))
+    else:
+        st = load_library().int8_quantize_bf16_routed(px, rows, K, pd, k, pc, ps, raw_stream(dev))
+    if st:
+        _err(st)
     return codes, scales
 
 
@@ -940,14 +960,18 @@ def moe_topk(logits, k, score="softmax", bias=None, groups=1, top_groups=1, grou
     (T, E), k, dev = logits.shape, int(k), logits.get_device()
     pl = _ptr(logits, logits.dtype, (T, E), "logits", dev)
     pb = None if bias is None else _ptr(bias, torch.float32, (E,), "bias", dev)
+    _, raw_stream, empty = _raw_calls()
     if out is None:
-        out = (logits.new_empty((T, max(k, 0)), dtype=torch.int32),
-               logits.new_empty((T, max(k, 0)), dtype=torch.float32))
-    ids, weights = out
-    pi = _ptr(ids, torch.int32, (T, max(k, 0)), "ids", dev)
-    pw = _ptr(weights, torch.float32, (T, max(k, 0)), "weights", dev)
-    _err(load_library().nvfp4_moe_topk(pl, logits.dtype is torch.bfloat16, T, E, k,
-                                       _SCORES[score], pb, int(groups), int(top_groups),
-                                       int(group_top), bool(renormalize), float(scale), pi, pw,
-                                       _raw_calls()[1](dev)))
+        n = k if k > 0 else 0  # a k that the library refuses
+        ids, weights = empty((T, n), (n, 1), torch.int32), empty((T, n), (n, 1), torch.float32)
+        pi, pw = ids.data_ptr(), weights.data_ptr()
+    else:
+        ids, weights = out
+        pi = _ptr(ids, torch.int32, (T, k), "ids", dev)
+        pw = _ptr(weights, torch.float32, (T, k), "weights", dev)
+    st = load_library().nvfp4_moe_topk(pl, logits.dtype is torch.bfloat16, T, E, k, _SCORES[score],
+                                       pb, groups, top_groups, group_top, bool(renormalize), scale,
+                                       pi, pw, raw_stream(dev))
+    if st:
+        _err(st)
     return ids, weights
