@@ -55,6 +55,7 @@ constexpr int KSTEPS = BKB / 32; // K = 32 per kind::i8 MMA
 constexpr int MAX_BT = 256;      // token columns of a tile
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_CHUNKS = 2;
+constexpr int MAX_SPLIT_BT = 128;  // token columns of a split tile at most
 constexpr int MAX_SPLIT = 4;     // pairs of a split tile (8 CTAs: the portable cluster size)
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int FIRST_EPI_WARP = 2;
@@ -459,20 +460,28 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 const int n = n0 + 32 * q + 8 * i + g;
                 sw[i] = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
             }
+            // lane l: token l of each of the warp's chunks (in hand before the accumulator is)
+            float sa_lane[MAX_BT / 64];
+#pragma unroll
+            for (int i = 0; i < MAX_BT / 64; ++i) {
+                const int j = half * 32 + i * 64 + lane;
+                sa_lane[i] = j < tl.rows ? __ldg(sA + tl.m0 + j) : 0.f;
+            }
             const int buf = tc & 1;
             if (!wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
-            for (int c = half * 32; c < tl.rows; c += 64) {
+#pragma unroll
+            for (int cc = 0; cc < MAX_BT / 64; ++cc) {
+                const int c = half * 32 + cc * 64;
+                if (c >= tl.rows) break;
                 uint32_t r[32];  // [channels 0-15, 16-31][8 tokens][row g, row g + 8][2 tokens]
                 tmem_ld_16x256b_x4(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
                 tmem_ld_16x256b_x4(acc + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
                 float sa[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = c + 8 * (i >> 1) + p2 + (i & 1);
-                    sa[i] = j < tl.rows ? __ldg(sA + tl.m0 + j) : 0.f;
-                }
+                for (int i = 0; i < 8; ++i)
+                    sa[i] = __shfl_sync(0xffffffffu, sa_lane[cc], 8 * (i >> 1) + p2 + (i & 1));
                 tmem_ld_wait();
                 reg_fence(r);
                 named_bar_sync(1 + half, 128);  // the buffer's last chunk has left
@@ -513,7 +522,9 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(&sm.acc_empty[buf], lead);
+            // (a buffer that no later tile takes is not handed back: every remote arrive is
+            // one that the MMA warp waits for, so none can reach a CTA that has left)
+            if (lane == 0 && t + 2 * nclusters < tiles) mbar_arrive_remote(&sm.acc_empty[buf], lead);
         }
     } else {
         // ------------------------------------------------------------ epilogue, split tiles
@@ -529,6 +540,10 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             const int my_cols = max(0, min(cw, tl.rows - part * cw));
             const int n = tl.n0 + (int)prank * BW + ch;
             const float sw = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
+            // lane l: the scales of this pair's tokens l and 32 + l (a share is at most 64)
+            const int m0 = tl.m0 + part * cw;
+            const float sa0 = lane < my_cols ? __ldg(sA + m0 + lane) : 0.f;
+            const float sa1 = 32 + lane < my_cols ? __ldg(sA + m0 + 32 + lane) : 0.f;
             if (tid == 0) mbar_arrive_expect_tx(&sm.red_full, s.split * ((my_cols + 3) / 4) * BW * 16);
             const int buf = tc & 1;
             if (!wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI)) break;
@@ -558,7 +573,9 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(&sm.acc_empty[buf], lead);
+            // (a buffer that no later tile takes is not handed back: every remote arrive is
+            // one that the MMA warp waits for, so none can reach a CTA that has left)
+            if (lane == 0 && t + 2 * nclusters < tiles) mbar_arrive_remote(&sm.acc_empty[buf], lead);
             if (!wait_bar<true>(&sm.red_full, tc & 1, abort, ROLE_EPI)) break;
             for (int c = tid / BW; c * 4 < my_cols; c += NUM_EPI_WARPS * 32 / BW) {
                 int4 v = make_int4(0, 0, 0, 0);
@@ -571,11 +588,12 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 }
                 const int sum[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c * 4 + j < my_cols && n < s.N) {
-                        const int m = tl.m0 + part * cw + c * 4 + j;
-                        Y[(size_t)m * s.N + n] = __float2bfloat16_rn((float)sum[j] * (sw * __ldg(sA + m)));
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int col = c * 4 + j;
+                    const float sa = __shfl_sync(0xffffffffu, col < 32 ? sa0 : sa1, col & 31);
+                    if (col < my_cols && n < s.N)
+                        Y[(size_t)(m0 + col) * s.N + n] = __float2bfloat16_rn((float)sum[j] * (sw * sa));
+                }
             }
             __syncwarp();
             if (t + nclusters < tiles && lane < s.split)
@@ -584,8 +602,11 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
     }
 
     // No CTA of a cluster leaves (or frees a pair's TMEM) while another may still use it.
+    // Nothing is published here: a release would wait for the output stores (1 to 2 us).
+    __syncwarp();
     tc_fence_before();
-    cluster_sync();
+    cluster_arrive_relaxed();
+    cluster_wait();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, tmem_cols(s.bt));
 }

@@ -1422,7 +1422,7 @@ Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
                                      : 0.5 * ((double)live * ((avg + c - 1) / c) +
                                               std::max<double>(live, (double)M / c + 0.5 * live));
         for (int sp = 1; sp <= i8::MAX_SPLIT; ++sp) {
-            if (sp > 1 && (bound * nblk > slots.clusters[sp] || steps < 2 * sp || c > 128)) break;
+            if (sp > 1 && (bound * nblk > slots.clusters[sp] || steps < 2 * sp || c > i8::MAX_SPLIT_BT)) break;
             const double per = (steps + sp - 1) / sp * std::max(0.150, 0.100 + 0.00087 * c);
             const double w = blocks * nblk / slots.clusters[sp];
             // few waves end with a partly idle one; many even out (experts differ in size)
