@@ -769,50 +769,62 @@ class GroupedSchedule:
 
 # --- INT8 products, their quantiser and the router -----------------------------------
 #
-# These are called once per layer and token batch, so the marshalling is kept short: one
-# test per tensor, and the current device and stream looked up without building objects.
+# These are called once per layer and token batch and often take less time on the GPU than
+# their marshalling here, so it is kept short: one look at each tensor, and the current
+# device, the current stream and the outputs' memory without building objects on the way.
 
-_raw = None
+class _Host:
+    """What the calls below look up once: torch's types and plain calls for the current
+    device index, a device index's current raw stream, and an uninitialised contiguous
+    tensor (size, stride, dtype) on the current device."""
 
-
-def _raw_calls():
-    """Three plain calls: the current device index, a device index's current raw stream, and
-    an uninitialised contiguous tensor (size, stride, dtype) on the current device."""
-    global _raw
-    if _raw is None:
+    def __init__(self):
         torch = _torch()
         c = torch._C
+        self.Tensor = torch.Tensor
+        self.i8, self.i32, self.f32, self.bf16 = torch.int8, torch.int32, torch.float32, torch.bfloat16
         if hasattr(c, "_cuda_getDevice") and hasattr(c, "_cuda_getCurrentRawStream"):
-            get = (c._cuda_getDevice, c._cuda_getCurrentRawStream)
+            self.device, self.stream = c._cuda_getDevice, c._cuda_getCurrentRawStream
         else:
-            get = (torch.cuda.current_device, lambda i: torch.cuda.current_stream(i).cuda_stream)
-        empty = getattr(getattr(getattr(c, "_dynamo", None), "guards", None),
-                        "_empty_strided_cuda", None)
-        if empty is None:
-            def empty(size, stride, dtype):
-                return torch.empty(size, dtype=dtype, device="cuda")
-        _raw = get + (empty,)
-    return _raw
+            self.device = torch.cuda.current_device
+            self.stream = lambda i: torch.cuda.current_stream(i).cuda_stream
+        self.empty = getattr(getattr(getattr(c, "_dynamo", None), "guards", None),
+                             "_empty_strided_cuda", None)
+        if self.empty is None:
+            self.empty = lambda size, stride, dtype: torch.empty(size, dtype=dtype, device="cuda")
+        lib = load_library()
+        self.gemm, self.grouped = lib.gemm_int8_w8a8, lib.gemm_int8_w8a8_grouped
+        self.quantize, self.routed = lib.int8_quantize_bf16, lib.int8_quantize_bf16_routed
+        self.topk = lib.nvfp4_moe_topk
+
+
+_host_calls = None
+
+
+def _host():
+    global _host_calls
+    if _host_calls is None:
+        _host_calls = _Host()
+    return _host_calls
 
 
 def _elsewhere(t, stream):
-    """The context a call has to enter first, or None: the tensors' device becomes current,
-    and what the call allocates belongs to the stream that uses it."""
+    """The context a call enters first when a stream is given or the tensors' device is not
+    the current one: that device becomes current, and what the call allocates belongs to
+    the stream that uses it."""
     torch = _torch()
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.is_cuda and t.get_device() != _raw_calls()[0]():
+    if stream is None:
         return torch.cuda.device(t.device)
-    return None
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t, dtype, shape, name, dev):
     """t's address; raises unless t is a contiguous `dtype` tensor of `shape` on CUDA device
     index `dev`."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and dev >= 0
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
                 and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
@@ -821,33 +833,29 @@ def _ptr(t, dtype, shape, name, dev):
     raise ValueError(f"{name} must be on CUDA device {dev}, got {t.device}")
 
 
-def _is_matrix(t, dims=2):
-    return isinstance(t, _torch().Tensor) and t.dim() == dims
-
-
 def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
     """Y[M,N] (bf16) = sA[m] * sW[n] * A . W^T: INT8 codes A [M,K], W [N,K] with one
     float32 scale per token (sA [M]) and per output channel (sW [N]); exact INT32 sums
     (K a multiple of 16, at most 131056)."""
-    torch = _torch()
-    if not _is_matrix(A) or not _is_matrix(W):
+    h = _host_calls or _host()
+    if not (isinstance(A, h.Tensor) and isinstance(W, h.Tensor) and A.dim() == 2 == W.dim()):
         raise TypeError("A and W must be 2-D torch.Tensors")
-    ctx = _elsewhere(A, stream)
-    if ctx is not None:
-        with ctx:
+    dev = A.get_device()
+    if stream is not None or (dev >= 0 and dev != h.device()):
+        with _elsewhere(A, stream):
             return gemm_int8_w8a8(A, sA, W, sW, out)
-    (M, K), N, dev = A.shape, W.shape[0], A.get_device()
-    pa = _ptr(A, torch.int8, (M, K), "A", dev)
-    psa = _ptr(sA, torch.float32, (M,), "sA", dev)
-    pw = _ptr(W, torch.int8, (N, K), "W", dev)
-    psw = _ptr(sW, torch.float32, (N,), "sW", dev)
-    _, raw_stream, empty = _raw_calls()
+    M, K = A.shape
+    N = W.shape[0]
+    pa = _ptr(A, h.i8, (M, K), "A", dev)
+    psa = _ptr(sA, h.f32, (M,), "sA", dev)
+    pw = _ptr(W, h.i8, (N, K), "W", dev)
+    psw = _ptr(sW, h.f32, (N,), "sW", dev)
     if out is None:
-        out = empty((M, N), (N, 1), torch.bfloat16)
+        out = h.empty((M, N), (N, 1), h.bf16)
         py = out.data_ptr()
     else:
-        py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
-    st = load_library().gemm_int8_w8a8(pa, psa, pw, psw, py, M, N, K, raw_stream(dev))
+        py = _ptr(out, h.bf16, (M, N), "out", dev)
+    st = h.gemm(pa, psa, pw, psw, py, M, N, K, h.stream(dev))
     if st:
         _err(st)
     return out
@@ -857,58 +865,29 @@ def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
     """The experts' INT8 products: rows offsets[e] .. offsets[e+1]-1 of A (INT8 [M,K], sA
     float32 [M]) times W[e] (INT8 [E,N,K], sW float32 [E,N]).  offsets: CUDA int32 [E+1]
     as moe_route returns it, read on the device.  Rows from offsets[E] on are not written."""
-    torch = _torch()
-    if not _is_matrix(A) or not _is_matrix(W, 3):
+    h = _host_calls or _host()
+    if not (isinstance(A, h.Tensor) and isinstance(W, h.Tensor) and A.dim() == 2 and W.dim() == 3):
         raise TypeError("A must be a 2-D and W a 3-D torch.Tensor")
-    ctx = _elsewhere(A, stream)
-    if ctx is not None:
-        with ctx:
+    dev = A.get_device()
+    if stream is not None or (dev >= 0 and dev != h.device()):
+        with _elsewhere(A, stream):
             return gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out)
-    (M, K), (E, N, _), dev = A.shape, W.shape, A.get_device()
-    pa = _ptr(A, torch.int8, (M, K), "A", dev)
-    psa = _ptr(sA, torch.float32, (M,), "sA", dev)
-    pw = _ptr(W, torch.int8, (E, N, K), "W", dev)
-    psw = _ptr(sW, torch.float32, (E, N), "sW", dev)
-    po = _ptr(offsets, torch.int32, (E + 1,), "offsets", dev)
-    _, raw_stream, empty = _raw_calls()
+    M, K = A.shape
+    E, N, _ = W.shape
+    pa = _ptr(A, h.i8, (M, K), "A", dev)
+    psa = _ptr(sA, h.f32, (M,), "sA", dev)
+    pw = _ptr(W, h.i8, (E, N, K), "W", dev)
+    psw = _ptr(sW, h.f32, (E, N), "sW", dev)
+    po = _ptr(offsets, h.i32, (E + 1,), "offsets", dev)
     if out is None:
-        out = empty((M, N), (N, 1), torch.bfloat16)
+        out = h.empty((M, N), (N, 1), h.bf16)
         py = out.data_ptr()
     else:
-        py = _ptr(out, torch.bfloat16, (M, N), "out", dev)
-    st = load_library().gemm_int8_w8a8_grouped(pa, psa, pw, psw, po, E, M, py, N, K, raw_stream(dev))
+        py = _ptr(out, h.bf16, (M, N), "out", dev)
+    st = h.grouped(pa, psa, pw, psw, po, E, M, py, N, K, h.stream(dev))
     if st:
         _err(st)
     return out
-
-
-def _int8_quantize(x, dest, k, out, stream):
-    torch = _torch()
-    if not _is_matrix(x):
-        raise TypeError("x must be a 2-D torch.Tensor")
-    ctx = _elsewhere(x, stream)
-    if ctx is not None:
-        with ctx:
-            return _int8_quantize(x, dest, k, out, None)
-    (rows, K), dev = x.shape, x.get_device()
-    n = rows if dest is None else rows * k
-    px = _ptr(x, torch.bfloat16, (rows, K), "x", dev)
-    pd = None if dest is None else _ptr(dest, torch.int32, (n,), "dest", dev)
-    _, raw_stream, empty = _raw_calls()
-    if out is None:
-        codes, scales = empty((n, K), (K, 1), torch.int8), empty((n,), (1,), torch.float32)
-        pc, ps = codes.data_ptr(), scales.data_ptr()
-    else:
-        codes, scales = out
-        pc = _ptr(codes, torch.int8, (n, K), "codes", dev)
-        ps = _ptr(scales, torch.float32, (n,), "scales", dev)
-    if dest is None:
-        st = load_library().int8_quantize_bf16(px, rows, K, pc, ps, raw_stream(dev))
-    else:
-        st = load_library().int8_quantize_bf16_routed(px, rows, K, pd, k, pc, ps, raw_stream(dev))
-    if st:
-        _err(st)
-    return codes, scales
 
 
 def int8_quantize_bf16(x, out=None, stream=None):
@@ -916,7 +895,20 @@ def int8_quantize_bf16(x, out=None, stream=None):
     amax/127 (1 for a row of zeros; NaN, with zero codes, for a row with an Inf or NaN),
     codes = 127 x / amax rounded half to even.  K a multiple of 16.  `out`, if given, is
     such a tuple of preallocated tensors."""
-    return _int8_quantize(x, None, 1, out, stream)
+    h = _host_calls or _host()
+    if not (isinstance(x, h.Tensor) and x.dim() == 2):
+        raise TypeError("x must be a 2-D torch.Tensor")
+    dev = x.get_device()
+    if stream is not None or (dev >= 0 and dev != h.device()):
+        with _elsewhere(x, stream):
+            return int8_quantize_bf16(x, out)
+    rows, K = x.shape
+    px = _ptr(x, h.bf16, (rows, K), "x", dev)
+    codes, scales, pc, ps = _int8_rows(h, rows, K, out, dev)
+    st = h.quantize(px, rows, K, pc, ps, h.stream(dev))
+    if st:
+        _err(st)
+    return codes, scales
 
 
 def int8_quantize_bf16_routed(x, dest, k=1, out=None, stream=None):
@@ -924,12 +916,33 @@ def int8_quantize_bf16_routed(x, dest, k=1, out=None, stream=None):
     rows in an MoE dispatch's order.  `dest` is the int32 [rows*k] CUDA tensor moe_route
     returns; entries outside [0, rows*k) are left out.  Returns (codes int8 [rows*k, K],
     scales float32 [rows*k])."""
-    if dest is None:
-        raise TypeError("dest must be a torch.Tensor")
+    h = _host_calls or _host()
+    if not (isinstance(x, h.Tensor) and x.dim() == 2):
+        raise TypeError("x must be a 2-D torch.Tensor")
     k = int(k)
     if k < 1:
         raise ValueError(f"k must be >= 1, got {k}")
-    return _int8_quantize(x, dest, k, out, stream)
+    dev = x.get_device()
+    if stream is not None or (dev >= 0 and dev != h.device()):
+        with _elsewhere(x, stream):
+            return int8_quantize_bf16_routed(x, dest, k, out)
+    rows, K = x.shape
+    px = _ptr(x, h.bf16, (rows, K), "x", dev)
+    pd = _ptr(dest, h.i32, (rows * k,), "dest", dev)
+    codes, scales, pc, ps = _int8_rows(h, rows * k, K, out, dev)
+    st = h.routed(px, rows, K, pd, k, pc, ps, h.stream(dev))
+    if st:
+        _err(st)
+    return codes, scales
+
+
+def _int8_rows(h, n, K, out, dev):
+    if out is None:
+        codes, scales = h.empty((n, K), (K, 1), h.i8), h.empty((n,), (1,), h.f32)
+        return codes, scales, codes.data_ptr(), scales.data_ptr()
+    codes, scales = out
+    return (codes, scales, _ptr(codes, h.i8, (n, K), "codes", dev),
+            _ptr(scales, h.f32, (n,), "scales", dev))
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -945,33 +958,33 @@ def moe_topk(logits, k, score="softmax", bias=None, groups=1, top_groups=1, grou
     of their group_top (1 or 2) best choices take part.  ids are in descending order of the
     choice, ties to the lowest index; weights are the chosen scores, divided by their sum
     if renormalize, times scale.  A NaN logit counts as -Inf."""
-    torch = _torch()
-    if not _is_matrix(logits):
+    h = _host_calls or _host()
+    if not (isinstance(logits, h.Tensor) and logits.dim() == 2):
         raise TypeError("logits must be a 2-D torch.Tensor")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    dtype = logits.dtype
+    if dtype is not h.f32 and dtype is not h.bf16:
+        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    ctx = _elsewhere(logits, stream)
-    if ctx is not None:
-        with ctx:
+    dev = logits.get_device()
+    if stream is not None or (dev >= 0 and dev != h.device()):
+        with _elsewhere(logits, stream):
             return moe_topk(logits, k, score, bias, groups, top_groups, group_top, renormalize,
                             scale, out)
-    (T, E), k, dev = logits.shape, int(k), logits.get_device()
-    pl = _ptr(logits, logits.dtype, (T, E), "logits", dev)
-    pb = None if bias is None else _ptr(bias, torch.float32, (E,), "bias", dev)
-    _, raw_stream, empty = _raw_calls()
+    T, E = logits.shape
+    k = int(k)
+    pl = _ptr(logits, dtype, (T, E), "logits", dev)
+    pb = None if bias is None else _ptr(bias, h.f32, (E,), "bias", dev)
     if out is None:
         n = k if k > 0 else 0  # a k that the library refuses
-        ids, weights = empty((T, n), (n, 1), torch.int32), empty((T, n), (n, 1), torch.float32)
+        ids, weights = h.empty((T, n), (n, 1), h.i32), h.empty((T, n), (n, 1), h.f32)
         pi, pw = ids.data_ptr(), weights.data_ptr()
     else:
         ids, weights = out
-        pi = _ptr(ids, torch.int32, (T, k), "ids", dev)
-        pw = _ptr(weights, torch.float32, (T, k), "weights", dev)
-    st = load_library().nvfp4_moe_topk(pl, logits.dtype is torch.bfloat16, T, E, k, _SCORES[score],
-                                       pb, groups, top_groups, group_top, bool(renormalize), scale,
-                                       pi, pw, raw_stream(dev))
+        pi = _ptr(ids, h.i32, (T, k), "ids", dev)
+        pw = _ptr(weights, h.f32, (T, k), "weights", dev)
+    st = h.topk(pl, dtype is h.bf16, T, E, k, _SCORES[score], pb, groups, top_groups, group_top,
+                bool(renormalize), scale, pi, pw, h.stream(dev))
     if st:
         _err(st)
     return ids, weights

@@ -309,14 +309,6 @@ __device__ __forceinline__ void cluster_sync() {
                  ::: "memory");
 }
 
-// The halves of a cluster barrier that publishes no memory writes.
-__device__ __forceinline__ void cluster_arrive_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // The shared::cluster address of the same smem location in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
     uint32_t r;
