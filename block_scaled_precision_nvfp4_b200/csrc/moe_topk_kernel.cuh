@@ -17,14 +17,16 @@
 // compared as they are.  Otherwise the choices are computed in FP32 with a proven error
 // bound; the list of the best is extended until nothing outside it can belong to the first
 // k, and where two neighbours are closer than the bound allows, it is ranked again by
-// 64-bit choices, one list entry per lane.  What that cannot settle (sums of a softmax,
-// groups closer than the bound, more near-ties than lanes) goes through the whole token
-// in 64 bits.  Weights are always 64-bit values of the k chosen scores, rounded once.
+// 64-bit choices, one list entry per lane.  What that cannot settle (groups closer than
+// the bound, more near-ties than lanes) goes through the whole token in 64 bits.  Weights are always 64-bit values of the k chosen scores, rounded once.
 //
 // One warp per token; a group's experts sit on `lpg` neighbouring lanes, V per lane, in
 // ascending order, so the lowest lane and the lowest slot hold the lowest index.  Few
-// bytes, many instructions: 8192 tokens over 256 experts in 8 groups (8.9 MB, 1.4 us of
-// HBM) are bound by the issue slots of the k selection rounds.
+// bytes, many instructions: bound by the integer and compare pipe (80 % of its rate).
+// 8192 tokens over 256 experts in 8 groups (8.9 MB, 1.4 us of HBM) take 12.0 us, 65536 of
+// them 74 us; everything in 64 bits took 28.8 us, selection rounds over all of a lane's
+// experts instead of the packed list 14.8 us (but for up to 2 experts per lane they are the
+// faster form: 64 experts 5.5 against 6.0 us).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -47,6 +49,7 @@ struct Params {
     int renorm;
     float scale;
     int per, lpg;    // experts of a group, lanes of a group
+    int lanes;       // lanes that hold at least one expert of the kept groups
     int vec;         // every lane's run of logits starts on a 16-byte (BF16: 8-byte) boundary
 };
 
@@ -214,7 +217,7 @@ __device__ __forceinline__ void load_logits(const X* __restrict__ row, int e0, i
 }
 
 template <int V, typename X>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, V <= 8 ? 8 : 4)
 moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
                 int32_t* __restrict__ ids, float* __restrict__ weights,
                 const __grid_constant__ Params p) {
@@ -304,55 +307,116 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         }
     }
 
-    // The lane's experts in descending order (a stable network: equal keys keep their
-    // order), then selection rounds: the best head of all lanes leaves its list, and lane j
-    // takes the j-th; a few more than k while they are too close to the k-th.
     uint32_t key[V];
-    int slot[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        key[v] = kept && v < cnt ? order_key(c[v]) : 0u;
-        slot[v] = e0 + v;
-    }
-#pragma unroll
-    for (int i = 0; i + 1 < V; ++i)
-#pragma unroll
-        for (int j = V - 1; j > i; --j) {
-            const bool swap = key[j] > key[j - 1];
-            const uint32_t hi = max(key[j], key[j - 1]), lo = min(key[j], key[j - 1]);
-            const int a = swap ? slot[j] : slot[j - 1], b = swap ? slot[j - 1] : slot[j];
-            key[j - 1] = hi, key[j] = lo;
-            slot[j - 1] = a, slot[j] = b;
-        }
-    uint32_t my_key = 0, kth = 0, last = 0;
+    for (int v = 0; v < V; ++v) key[v] = kept && v < cnt ? order_key(c[v]) : 0u;
+
+    // The list of the best, in descending order: lane j holds the j-th; n entries, and none
+    // outside it can belong to the first k (unless n == 32, see below).
+    uint32_t my_key = 0;
     int my_id = 0, n = 0;
-    auto take = [&](uint32_t top) {
-        const int src = __ffs(__ballot_sync(FULL, key[0] == top)) - 1;
-        const int id = __shfl_sync(FULL, slot[0], src);
-        if (lane == n) {
-            my_key = top;
-            my_id = id;
-        }
-        const bool pop = lane == src;
+    bool complete = false;
+    __shared__ uint2 list[WARPS][32];
+    if (V >= 4 && p.k <= p.lanes) {
+        // The k-th largest of the lanes' maxima is no larger than the k-th choice.  What
+        // reaches it (with a bias: reaches within the gap below it) is a short list, which
+        // is packed in index order and ranked by counting.
+        uint32_t m = 0, t0 = 0;
 #pragma unroll
-        for (int v = 0; v + 1 < V; ++v) {
-            key[v] = pop ? key[v + 1] : key[v];
-            slot[v] = pop ? slot[v + 1] : slot[v];
+        for (int v = 0; v < V; ++v) m = max(m, key[v]);
+        for (int j = 0; j < p.k; ++j) {
+            t0 = __reduce_max_sync(FULL, m);
+            m = m == t0 ? 0u : m;
         }
-        if (pop) key[V - 1] = 0;
-        last = top;
-        ++n;
-    };
-    while (n < p.k) take(__reduce_max_sync(FULL, key[0]));  // k experts are kept at least
-    kth = last;
-    if (bias) {
-        // experts out of reach of the k-th end the list; so does one equal to it without
-        // rounding (two infinities), where the index has decided already
-        const float a = key_value(kth);
-        while (n < 32) {
-            const uint32_t top = __reduce_max_sync(FULL, key[0]);
-            if (top == 0 || !(a - key_value(top) <= gap(a, p.sigmoid != 0))) break;
-            take(top);
+        if (bias) {
+            const float a = key_value(t0);
+            t0 = order_key(fmaxf(a - gap(a, p.sigmoid != 0), -INFINITY));
+        }
+        t0 = max(t0, 1u);
+        int mine = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) mine += key[v] >= t0;
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(FULL, at, o);
+            if (lane >= o) at += x;
+        }
+        n = __shfl_sync(FULL, at, 31);
+        if (n <= 32) {
+            at -= mine;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (key[v] >= t0) list[warp][at++] = make_uint2(key[v], (uint32_t)(e0 + v));
+            __syncwarp();
+            const uint2 e = lane < n ? list[warp][lane] : make_uint2(0u, 0u);
+            int r = 0;
+            for (int j = 0; j < n; ++j) {
+                const uint32_t o = __shfl_sync(FULL, e.x, j);
+                r += o > e.x || (o == e.x && j < lane);
+            }
+            __syncwarp();
+            if (lane < n) list[warp][r] = e;
+            __syncwarp();
+            if (lane < n) {
+                my_key = list[warp][lane].x;
+                my_id = (int)list[warp][lane].y;
+            }
+            complete = true;
+        }
+    }
+    if (!complete) {
+        // Fewer lanes than k in the kept groups, or many equal choices: each lane's experts
+        // in descending order (a stable network: equal keys keep their order), then
+        // selection rounds: the best head of all lanes leaves its list; a few more than k
+        // rounds while they are too close to the k-th.
+        int slot[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) slot[v] = e0 + v;
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i)
+#pragma unroll
+            for (int j = V - 1; j > i; --j) {
+                const bool swap = key[j] > key[j - 1];
+                const uint32_t hi = max(key[j], key[j - 1]), lo = min(key[j], key[j - 1]);
+                const int a = swap ? slot[j] : slot[j - 1], b = swap ? slot[j - 1] : slot[j];
+                key[j - 1] = hi, key[j] = lo;
+                slot[j - 1] = a, slot[j] = b;
+            }
+        n = 0;
+        uint32_t kth = 0;
+        auto take = [&](uint32_t top) {
+            const int src = __ffs(__ballot_sync(FULL, key[0] == top)) - 1;
+            const int id = __shfl_sync(FULL, slot[0], src);
+            if (lane == n) {
+                my_key = top;
+                my_id = id;
+            }
+            const bool pop = lane == src;
+#pragma unroll
+            for (int v = 0; v + 1 < V; ++v) {
+                key[v] = pop ? key[v + 1] : key[v];
+                slot[v] = pop ? slot[v + 1] : slot[v];
+            }
+            if (pop) key[V - 1] = 0;
+            if (n == p.k - 1) kth = top;
+            ++n;
+        };
+        while (n < p.k) take(__reduce_max_sync(FULL, key[0]));  // k experts are kept at least
+        complete = true;
+        if (bias) {
+            // experts out of reach of the k-th end the list; so does one equal to it without
+            // rounding (two infinities), where the index has decided already
+            const float a = key_value(kth);
+            while (true) {
+                const uint32_t top = __reduce_max_sync(FULL, key[0]);
+                if (top == 0 || !(a - key_value(top) <= gap(a, p.sigmoid != 0))) break;
+                if (n == 32) {
+                    complete = false;
+                    break;
+                }
+                take(top);
+            }
         }
     }
     bool near = false;
@@ -360,10 +424,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         const uint32_t next = __shfl_down_sync(FULL, my_key, 1);
         const float a = key_value(my_key);
         near = __any_sync(FULL, lane + 1 < n && a - key_value(next) <= gap(a, p.sigmoid != 0));
-        const float k0 = key_value(kth);
-        const bool more = n == 32 && p.k < 32 && k0 - key_value(last) <= gap(k0, p.sigmoid != 0);
-        const bool full = p.k == 32 && __reduce_max_sync(FULL, key[0]) != 0;  // no lane to look further
-        if (more || full || (near && !p.sigmoid)) {
+        if (!complete) {
             topk_exact<V, X>(logits, bias, ids, weights, p, t);
             return;
         }
@@ -378,10 +439,26 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         x = (double)f;
         sc = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : f > -INFINITY ? exp(x - (double)xmax) : 0.0;
     }
+    double sum64 = (double)sum;
+    if (near && !p.sigmoid) {  // the softmax's sum in 64 bits too
+        float f[V];
+        load_logits<V, X>(row, e0, cnt, p.vec != 0, f);
+        sum64 = 0.0;
+#pragma unroll 1
+        for (int v = 0; v < V; ++v) {
+            float q = f[0];
+#pragma unroll
+            for (int u = 1; u < V; ++u) q = u == v ? f[u] : q;
+            if (q > -INFINITY) sum64 += exp((double)q - (double)xmax);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum64 += __shfl_xor_sync(FULL, sum64, o);
+    }
     int rank = lane;
     if (near) {
         const double NEG = -__longlong_as_double(0x7FF0000000000000ll);
-        double ch = live ? sc + (double)__ldg(bias + my_id) : NEG;
+        const double s64 = p.sigmoid ? sc : sum64 > 0.0 ? sc / sum64 : 0.0;
+        double ch = live ? s64 + (double)__ldg(bias + my_id) : NEG;
         if (!(ch == ch)) ch = NEG;
         rank = 0;
         for (int i = 0; i < n; ++i) {
@@ -398,7 +475,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(FULL, total, o);
         w = total > 0.0 ? sc / total : 0.0;
     } else if (!p.sigmoid) {
-        w = sum > 0.f ? sc / (double)sum : 0.0;
+        w = sum64 > 0.0 ? sc / sum64 : 0.0;
     }
     if (chosen) {
         ids[(size_t)t * p.k + rank] = my_id;

@@ -1477,7 +1477,7 @@ nvfp4_status launch_int8(const int8_t* A, const float* sA, const int8_t* W, cons
     Int8Slots slots;
     if ((st = int8_slots(dev, info, slots)) != NVFP4_OK) return st;
     const Int8Plan p = int8_plan(M, N, K, E, slots);
-    if (p.tiles > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "M x N too large");
+    if (p.tiles > (1 << 30)) return fail(NVFP4_ERR_INVALID_ARG, "M x N too large");
     CUtensorMap tmW, tmA;
     if ((st = make_map_u8(&tmW, W, (uint64_t)K, (uint64_t)E * N, i8::BKB, i8::BW)) != NVFP4_OK) return st;
     if ((st = make_map_u8(&tmA, A, (uint64_t)K, (uint64_t)M, i8::BKB,
@@ -1611,9 +1611,11 @@ nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, i
         return fail(NVFP4_ERR_NOPATH, "the router is compiled for sm_100 only (device sm_%d)", info.sm_arch);
     if (T == 0) return ok();
     tk::Params p = {T, E, k, score == NVFP4_SCORE_SIGMOID, groups, top_groups, group_top,
-                    renormalize != 0, scale, per, 32, 0};
+                    renormalize != 0, scale, per, 32, 0, 0};
     while (p.lpg * groups > 32) p.lpg /= 2;  // a power of two of lanes for each group
     const int v = (per + p.lpg - 1) / p.lpg;
+    const int slots = v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : v <= 8 ? 8 : 16;  // experts of a lane
+    p.lanes = top_groups * ((per + slots - 1) / slots);
     p.vec = v > 2 && E % 4 == 0 && per % 4 == 0;  // runs of 4 or more
     const dim3 grid((unsigned)((T + tk::WARPS - 1) / tk::WARPS));
     cudaError_t e;
