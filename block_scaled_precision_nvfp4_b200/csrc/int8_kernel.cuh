@@ -269,6 +269,17 @@ __device__ __forceinline__ void plan_rows(Smem& sm, const Shape& s, const int32_
     }
 }
 
+// named_bar_sync that returns whether `ok` held in every thread.
+__device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all) : "r"(id), "r"(nthreads), "r"((uint32_t)ok) : "memory");
+    return all != 0;
+}
 // The halves of a cluster barrier that publishes no memory writes.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -404,6 +415,11 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             int tc = 0;
             Ring ring;
             bool ok = true;
+#ifdef NVFP4_WAIT_TEST
+            // test-only: wait for a commit that has not been issued, so that this bounded
+            // wait expires and every role of the cluster takes its abort path
+            if (g_wait_test_stall && !wait_bar(&sm.drain, 0, abort, ROLE_MMA)) ok = false;
+#endif
             // descriptors of stage 0; a stage further is sbytes / 16 more in the address field
             const uint64_t w_desc0 = desc_kmajor_sw128(smem_u32(stages));
             const uint64_t a_desc0 = desc_kmajor_sw128(smem_u32(stages) + CHUNKS * BW * BKB);
@@ -476,7 +492,9 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 sa_lane[i] = j < tl.rows ? __ldg(sA + tl.m0 + j) : 0.f;
             }
             const int buf = tc & 1;
-            if (!wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI)) break;
+            // a warp that gives up here still meets its three others at the next barrier,
+            // which tells all four
+            bool ok = wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI);
             tc_fence_after();
             const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
 #pragma unroll
@@ -484,15 +502,18 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 const int c = half * 32 + cc * 64;
                 if (c >= tl.rows) break;
                 uint32_t r[32];  // [channels 0-15, 16-31][8 tokens][row g, row g + 8][2 tokens]
-                tmem_ld_16x256b_x4(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-                tmem_ld_16x256b_x4(acc + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                if (ok) {
+                    tmem_ld_16x256b_x4(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                    tmem_ld_16x256b_x4(acc + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                }
                 float sa[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     sa[i] = __shfl_sync(0xffffffffu, sa_lane[cc], 8 * (i >> 1) + p2 + (i & 1));
                 tmem_ld_wait();
                 reg_fence(r);
-                named_bar_sync(1 + half, 128);  // the buffer's last chunk has left
+                ok = named_bar_and(1 + half, 128, ok);  // the buffer's last chunk has left
+                if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // 8 tokens
                     uint32_t m[4];             // 8 x 8 blocks of channels 0, 8, 16, 24
@@ -528,6 +549,7 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                     }
                 }
             }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             // (a buffer that no later tile takes is not handed back: every remote arrive is
