@@ -1395,8 +1395,10 @@ nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
 // pairs per tile, by the kernel's own measured costs (B200; M x 5376 x 14336):
 //   a 128-byte step of K   100 + 0.87 bt ns, at least 150   (64 tokens 156, 128 201, 256 322)
 //   the weights' bytes     6.2 TB/s
-//   a split tile           0.2 us + 45 ns per token for the exchange of sums
-//                          (64 tokens: 18.3 us on 3 pairs a tile, 21.5 unsplit)
+//   a tile                 0.25 us (512 x 8 rows over 64 experts [2816, 2048], memory-bound:
+//                          65 us in tiles of 128 tokens, 69 in tiles of 64)
+//   a split tile           0.2 us + 55 ns per token for the exchange of sums
+//                          (64 tokens: 18 us on 3 pairs a tile, 21.5 unsplit)
 //   a pair that takes part 8 ns
 // A split is taken only where all of its clusters run at once: with several split tiles
 // per cluster the exchange is not hidden (333 tokens: 43 us on 3 pairs a tile, 27 unsplit).
@@ -1414,13 +1416,13 @@ Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
     double best = 1e30;
     int bt = 32, split = 1;
     for (int c = 32; c <= i8::MAX_BT; c += 32) {
-        // of several groups, half and half: all of one size, or of many sizes, where half a
-        // block of each goes to its ragged end
+        // of several groups, between all of one size (0.3) and of many sizes, where half a
+        // block of each goes to its ragged end (0.7)
         const long long bound = blocks_at_most(c);
         const int avg = (M + live - 1) / live;
         const double blocks = E == 1 ? bound
-                                     : 0.5 * ((double)live * ((avg + c - 1) / c) +
-                                              std::max<double>(live, (double)M / c + 0.5 * live));
+                                     : 0.3 * live * ((avg + c - 1) / c) +
+                                           0.7 * std::max<double>(live, (double)M / c + 0.5 * live);
         for (int sp = 1; sp <= i8::MAX_SPLIT; ++sp) {
             if (sp > 1 && (bound * nblk > slots.clusters[sp] || steps < 2 * sp || c > i8::MAX_SPLIT_BT)) break;
             const double per = (steps + sp - 1) / sp * std::max(0.150, 0.100 + 0.00087 * c);
@@ -1428,9 +1430,9 @@ Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
             // few waves end with a partly idle one; many even out (experts differ in size)
             const double waves = E == 1 || w < 2 ? std::ceil(w) : w + 0.5;
             const double compute = waves * per;
-            const double us = std::max(compute, mem_us) + 0.15 * compute + 0.004 * c +
+            const double us = std::max(compute, mem_us) + 0.15 * compute + 0.25 * waves + 0.004 * c +
                               0.008 * sp * std::min<double>(bound * nblk, slots.clusters[sp]) +
-                              (sp > 1 ? 0.2 + 0.045 * std::min(c, M) : 0.0);
+                              (sp > 1 ? 0.2 + 0.055 * std::min(c, M) : 0.0);
             if (us < best) {
                 best = us;
                 bt = c;
