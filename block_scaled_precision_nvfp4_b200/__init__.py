@@ -770,13 +770,19 @@ class GroupedSchedule:
 # --- INT8 products, their quantiser and the router -----------------------------------
 #
 # These are called once per layer and token batch and often take less time on the GPU than
-# their marshalling here, so it is kept short: one look at each tensor, and the current
-# device, the current stream and the outputs' memory without building objects on the way.
+# their marshalling, so the plain case (tensors on the current device, no `out`, no
+# `stream`) goes through a small CPython module (csrc/host_calls.cpp).  It returns None for
+# everything else, which then takes the calls below: they do the same, and name what is
+# wrong.  Without the module (it is built against one torch version) they do all of it.
+
+def _no_fast_call(*args):
+    return None
+
 
 class _Host:
-    """What the calls below look up once: torch's types and plain calls for the current
-    device index, a device index's current raw stream, and an uninitialised contiguous
-    tensor (size, stride, dtype) on the current device."""
+    """What the calls below look up once: the module's calls, torch's types and plain calls
+    for the current device index, a device index's current raw stream, and an uninitialised
+    contiguous tensor (size, stride, dtype) on the current device."""
 
     def __init__(self):
         torch = _torch()
@@ -796,16 +802,25 @@ class _Host:
         self.gemm, self.grouped = lib.gemm_int8_w8a8, lib.gemm_int8_w8a8_grouped
         self.quantize, self.routed = lib.int8_quantize_bf16, lib.int8_quantize_bf16_routed
         self.topk = lib.nvfp4_moe_topk
+        self.fast_gemm = self.fast_grouped = self.fast_quantize = self.fast_topk = _no_fast_call
+        try:
+            from . import _host_calls as fast
+        except ImportError:
+            return
+        fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (self.gemm, self.grouped, self.quantize, self.routed, self.topk)))
+        self.fast_gemm, self.fast_grouped = fast.gemm, fast.grouped
+        self.fast_quantize, self.fast_topk = fast.quantize, fast.topk
 
 
-_host_calls = None
+_host_state = None
 
 
 def _host():
-    global _host_calls
-    if _host_calls is None:
-        _host_calls = _Host()
-    return _host_calls
+    global _host_state
+    if _host_state is None:
+        _host_state = _Host()
+    return _host_state
 
 
 def _elsewhere(t, stream):
@@ -837,7 +852,11 @@ def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
     """Y[M,N] (bf16) = sA[m] * sW[n] * A . W^T: INT8 codes A [M,K], W [N,K] with one
     float32 scale per token (sA [M]) and per output channel (sW [N]); exact INT32 sums
     (K a multiple of 16, at most 131056)."""
-    h = _host_calls or _host()
+    h = _host_state or _host()
+    if out is None and stream is None:
+        r = h.fast_gemm(A, sA, W, sW)
+        if r is not None:
+            return r if type(r) is not int else _err(r)
     if not (isinstance(A, h.Tensor) and isinstance(W, h.Tensor) and A.dim() == 2 == W.dim()):
         raise TypeError("A and W must be 2-D torch.Tensors")
     dev = A.get_device()
@@ -865,7 +884,11 @@ def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
     """The experts' INT8 products: rows offsets[e] .. offsets[e+1]-1 of A (INT8 [M,K], sA
     float32 [M]) times W[e] (INT8 [E,N,K], sW float32 [E,N]).  offsets: CUDA int32 [E+1]
     as moe_route returns it, read on the device.  Rows from offsets[E] on are not written."""
-    h = _host_calls or _host()
+    h = _host_state or _host()
+    if out is None and stream is None:
+        r = h.fast_grouped(A, sA, W, sW, offsets)
+        if r is not None:
+            return r if type(r) is not int else _err(r)
     if not (isinstance(A, h.Tensor) and isinstance(W, h.Tensor) and A.dim() == 2 and W.dim() == 3):
         raise TypeError("A must be a 2-D and W a 3-D torch.Tensor")
     dev = A.get_device()
@@ -895,7 +918,11 @@ def int8_quantize_bf16(x, out=None, stream=None):
     amax/127 (1 for a row of zeros; NaN, with zero codes, for a row with an Inf or NaN),
     codes = 127 x / amax rounded half to even.  K a multiple of 16.  `out`, if given, is
     such a tuple of preallocated tensors."""
-    h = _host_calls or _host()
+    h = _host_state or _host()
+    if out is None and stream is None:
+        r = h.fast_quantize(x)
+        if r is not None:
+            return r if type(r) is not int else _err(r)
     if not (isinstance(x, h.Tensor) and x.dim() == 2):
         raise TypeError("x must be a 2-D torch.Tensor")
     dev = x.get_device()
@@ -916,7 +943,11 @@ def int8_quantize_bf16_routed(x, dest, k=1, out=None, stream=None):
     rows in an MoE dispatch's order.  `dest` is the int32 [rows*k] CUDA tensor moe_route
     returns; entries outside [0, rows*k) are left out.  Returns (codes int8 [rows*k, K],
     scales float32 [rows*k])."""
-    h = _host_calls or _host()
+    h = _host_state or _host()
+    if out is None and stream is None:
+        r = h.fast_quantize(x, dest, k)
+        if r is not None:
+            return r if type(r) is not int else _err(r)
     if not (isinstance(x, h.Tensor) and x.dim() == 2):
         raise TypeError("x must be a 2-D torch.Tensor")
     k = int(k)
@@ -958,7 +989,12 @@ def moe_topk(logits, k, score="softmax", bias=None, groups=1, top_groups=1, grou
     of their group_top (1 or 2) best choices take part.  ids are in descending order of the
     choice, ties to the lowest index; weights are the chosen scores, divided by their sum
     if renormalize, times scale.  A NaN logit counts as -Inf."""
-    h = _host_calls or _host()
+    h = _host_state or _host()
+    if out is None and stream is None:
+        r = h.fast_topk(logits, k, _SCORES.get(score, -1), bias, groups, top_groups, group_top,
+                        renormalize, scale)
+        if r is not None:
+            return r if type(r) is not int else _err(r)
     if not (isinstance(logits, h.Tensor) and logits.dim() == 2):
         raise TypeError("logits must be a 2-D torch.Tensor")
     dtype = logits.dtype
