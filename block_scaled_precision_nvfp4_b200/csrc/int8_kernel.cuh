@@ -233,7 +233,7 @@ __device__ __forceinline__ Tile decode(const Smem& sm, const Shape& s, int t, in
 
 // The token blocks of every expert, from the offsets in device memory (or one group of
 // M rows without them).  Offsets that are not a non-decreasing run from 0 to at most M
-// give no tile at all and a device error bit.  One warp; bad is 0 on entry.
+// give no tile at all and a device error bit.  One warp.
 __device__ __forceinline__ void plan_rows(Smem& sm, const Shape& s, const int32_t* __restrict__ offsets) {
     const int lane = threadIdx.x & 31;
     int base = 0, bad = 0;
@@ -263,9 +263,9 @@ __device__ __forceinline__ void plan_rows(Smem& sm, const Shape& s, const int32_
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (bad && lane == 0) {
-        sm.bad = 1;
-        if (blockIdx.x == 0) atomicOr(&g_device_error, grouped_pair::BAD_OFFSETS);
+    if (lane == 0) {
+        sm.bad = bad;
+        if (bad && blockIdx.x == 0) atomicOr(&g_device_error, grouped_pair::BAD_OFFSETS);
     }
 }
 
@@ -346,7 +346,6 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         mbar_init(&sm.red_full, 1);
         mbar_init(&sm.red_free, s.split * NUM_EPI_WARPS);
         sm.abort = 0;
-        sm.bad = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmA);
@@ -355,16 +354,19 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         tmem_alloc_pair(&sm.tmem_base, tmem_cols(s.bt));
         tmem_relinquish_pair();
     }
-    __syncthreads();
+    if (!offsets && warp == FIRST_EPI_WARP) plan_rows(sm, s, offsets);
+    tc_fence_before();
+    cluster_sync();  // every CTA's barriers exist before any remote arrive
+    tc_fence_after();
     // The kernel behind this one may start its own set-up now: not earlier, so that its
     // tensor-memory allocation cannot come before this CTA's.
     grid_dependents_launch();
     // The set-up above overlaps the kernel before this one; its output is read only from here.
     grid_dependency_wait();
-    if (warp == FIRST_EPI_WARP) plan_rows(sm, s, offsets);
-    tc_fence_before();
-    cluster_sync();  // every CTA's barriers exist before any remote arrive
-    tc_fence_after();
+    if (offsets) {
+        if (warp == FIRST_EPI_WARP) plan_rows(sm, s, offsets);
+        __syncthreads();
+    }
     const uint32_t tmem = sm.tmem_base;
     const int tiles = sm.bad ? 0 : sm.tb_start[s.E] * nblk;
 
@@ -530,21 +532,48 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 }
                 named_bar_sync(1 + half, 128);
                 const int cnt = min(32, tl.rows - c);
-                const int n = n0 + (lane & 15) * 8;
+                if (wide) {
+                    const int n = n0 + (lane & 15) * 8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = q * 8 + i * 2 + (lane >> 4);
-                    const uint4 v = *reinterpret_cast<const uint4*>(
-                        out + tok * 256 + ((((lane & 15)) ^ (tok & 7)) << 4));
-                    if (tok < cnt) {
-                        uint16_t* y = reinterpret_cast<uint16_t*>(Y) + (size_t)(tl.m0 + c + tok) * s.N + n;
-                        if (wide) {
-                            if (n < s.N) *reinterpret_cast<uint4*>(y) = v;
-                        } else {
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = q * 8 + i * 2 + (lane >> 4);
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            out + tok * 256 + ((((lane & 15)) ^ (tok & 7)) << 4));
+                        if (tok < cnt && n < s.N)
+                            *reinterpret_cast<uint4*>(Y + (size_t)(tl.m0 + c + tok) * s.N + n) = v;
+                    }
+                } else {
+                    // Rows start anywhere: each leaves as the 16-byte pieces between its first
+                    // and last 16-byte boundaries and two bytes at a time around them.
+                    // (Two-byte stores alone took 24 us for 700 x 2500 x 6000, four-byte ones
+                    // 21.)  The second CTA's columns may all lie past N.
+                    const int width = max(0, min(BW, s.N - n0));
+                    const int piece = lane & 15;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (n + k < s.N) y[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = q * 8 + i * 2 + (lane >> 4);
+                        const uint8_t* const src = out + tok * 256;
+                        const int x = (tok & 7) << 4;  // a row's 16-byte blocks are exchanged by it
+                        uint16_t* const y = reinterpret_cast<uint16_t*>(Y) + (size_t)(tl.m0 + c + tok) * s.N + n0;
+                        // elements before the first boundary, whole pieces, and where they end
+                        const int head = min(width, (int)(-(reinterpret_cast<uintptr_t>(y) >> 1) & 7));
+                        const int tail = head + ((width - head) & ~7);
+                        const int e = head + piece * 8;
+                        uint32_t w[5];
+#pragma unroll
+                        for (int k = 0; k < 5; ++k) {
+                            const int byte = min((e >> 1) + k, BW / 2 - 1) * 4;
+                            w[k] = *reinterpret_cast<const uint32_t*>(src + (byte ^ x));
+                        }
+                        const int edge = piece < 8 ? piece : tail + piece - 8;  // one element of the ends
+                        const uint16_t h = *reinterpret_cast<const uint16_t*>(src + ((min(edge, BW - 1) * 2) ^ x));
+                        if (tok < cnt) {
+                            const uint32_t sh = (e & 1) * 16;
+                            if (e + 8 <= tail)
+                                *reinterpret_cast<uint4*>(y + e) =
+                                    make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                                               __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+                            if (piece < 8 ? edge < head : edge < width) y[edge] = h;
                         }
                     }
                 }

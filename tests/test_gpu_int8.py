@@ -205,6 +205,22 @@ def test_two_streams_at_once():
         assert torch.equal(_bits(y), _bits(got[i % len(cases)][0]))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (33, 127, 64), (40, 129, 64), (300, 131, 64), (257, 250, 64),
+                                   (100, 1001, 64), (64, 383, 64), (300, 515, 64), (70, 1285, 64),
+                                   (520, 254, 64), (31, 6, 64), (200, 2, 64), (5, 259, 4096)])
+def test_nothing_is_written_around_the_output(M, N, K):
+    """Every row start modulo 16 bytes, widths around the tile's; a frame around Y stays."""
+    rng = np.random.default_rng(M + N)
+    A, W, sA, sW = _codes(rng, M, K), _codes(rng, N, K), _scales(rng, M), _scales(rng, N)
+    frame = 4096
+    buf = torch.full((2 * frame + M * N + 8,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[frame:frame + M * N].view(M, N)
+    nv.gemm_int8_w8a8(_d(A), _d(sA), _d(W), _d(sW), out=out)
+    torch.cuda.synchronize()
+    _close(out, _ref(A, sA, W, sW))
+    assert (buf[:frame] == 9.0).all() and (buf[frame + M * N:] == 9.0).all()
+
+
 def test_python_refusals():
     z = lambda *s, dt=torch.int8: torch.zeros(s, dtype=dt, device="cuda")
     f = lambda *s: z(*s, dt=torch.float32)
