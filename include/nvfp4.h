@@ -12,7 +12,8 @@
  * nearest even).  The declared formats are never widened (module doc,
  * Invariants): a format pair that has neither a native kernel nor an exact
  * conversion here is reported as NVFP4_EXEC_NO_PATH, and every matmul entry
- * point refuses it.
+ * point refuses it.  Beside it stand INT8 products, their row quantiser and the router
+ * to experts; their sections give their own operations and layouts.
  *
  * Layouts (all row-major, contiguous, no padding):
  *   A      uint8 [M][K/2]   E2M1 codes, two per byte, even k in the low nibble
