@@ -95,10 +95,11 @@ PyObject* guarded(F&& body) {
 // Runs an entry point without the interpreter's lock (a launch can wait for a full queue).
 template <typename F>
 nvfp4_status unlocked(F&& call) {
-    PyThreadState* state = PyEval_SaveThread();
-    const nvfp4_status st = call();
-    PyEval_RestoreThread(state);
-    return st;
+    struct Unlock {
+        PyThreadState* state = PyEval_SaveThread();
+        ~Unlock() { PyEval_RestoreThread(state); }
+    } unlock;
+    return call();
 }
 
 PyObject* status(nvfp4_status st) { return PyLong_FromLong((long)st); }

@@ -273,6 +273,9 @@ W4a16LdgKern w4a16_ldg_kernel_for(int nb) {
     }
 }
 
+// Rows (tokens, channels) of the INT8 calls and the router: an int with a tile to spare.
+constexpr int kMaxRows = INT32_MAX - 1024;
+
 // A launch that may start while the stream's previous kernel finishes (the kernel waits
 // for it before it reads or writes memory).
 template <typename... P, typename... Args>
@@ -1459,7 +1462,9 @@ nvfp4_status launch_int8(const int8_t* A, const float* sA, const int8_t* W, cons
     if (K < 16 || K % 16 != 0 || K > i8::MAX_K)
         return fail(NVFP4_ERR_INVALID_ARG, "INT8 needs K a multiple of 16 in [16, %d] (got %d)",
                     i8::MAX_K, K);
-    if ((long long)E * N > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "E * N too large");
+    // row indexes of a tile that starts at the last row stay ints
+    if ((long long)E * N > kMaxRows || M > kMaxRows)
+        return fail(NVFP4_ERR_INVALID_ARG, "M and E * N must be at most %d", kMaxRows);
     if (M > 0 && N > 0) {
         if (!A || !sA || !W || !sW || !Y) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
         if (!aligned16(A) || !aligned16(W) || !aligned16(Y))
@@ -1530,7 +1535,8 @@ namespace {
 nvfp4_status int8_quantize_impl(const void* X, int rows, int K, const int32_t* dest, int k,
                                 int8_t* codes, float* scales, void* stream) {
     namespace q = nvfp4::int8q;
-    if (rows < 0) return fail(NVFP4_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+    if (rows < 0 || rows > kMaxRows)
+        return fail(NVFP4_ERR_INVALID_ARG, "rows must be in [0, %d] (got %d)", kMaxRows, rows);
     if (K < 16 || K % 16 != 0)
         return fail(NVFP4_ERR_INVALID_ARG, "K must be a positive multiple of 16 (got %d)", K);
     if (rows > 0) {
@@ -1583,7 +1589,8 @@ nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, i
                             int renormalize, float scale, int32_t* ids, float* weights,
                             void* stream) {
     namespace tk = nvfp4::topk;
-    if (T < 0) return fail(NVFP4_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+    if (T < 0 || T > kMaxRows)
+        return fail(NVFP4_ERR_INVALID_ARG, "T must be in [0, %d] (got %d)", kMaxRows, T);
     if (E < 1 || E > tk::MAX_EXPERTS)
         return fail(NVFP4_ERR_INVALID_ARG, "E must be in [1, %d] (got %d)", tk::MAX_EXPERTS, E);
     if (score != NVFP4_SCORE_SOFTMAX && score != NVFP4_SCORE_SIGMOID)

@@ -564,7 +564,7 @@ NVFP4_API nvfp4_status gemm_nvfp4_w4a4_grouped_packed_sched_combine(
  *
  * A [M][K] and W [N][K] are row-major int8 and Y [M][N] bf16, 16-byte aligned; sA
  * [M] and sW [N] are float, 4-byte aligned.  K is a multiple of 16, 16 <= K <= 131056
- * (the INT32 sum cannot overflow); M, N >= 0 are otherwise free.  Nothing is enqueued
+ * (the INT32 sum cannot overflow); M and N are otherwise free, 0 .. 2^31 - 1025.  Nothing is enqueued
  * for M == 0 or N == 0.  No workspace.  A and W may be the same buffer; Y may not
  * overlap an input. */
 NVFP4_API nvfp4_status gemm_int8_w8a8(const int8_t* A, const float* sA, const int8_t* W,
@@ -578,7 +578,7 @@ NVFP4_API nvfp4_status gemm_int8_w8a8(const int8_t* A, const float* sA, const in
  *                no host round trip and can be captured in a graph.  Rows of Y from
  *                offsets[E] on are left as they were.  Offsets that are not such a run
  *                write nothing at all and are reported by nvfp4_check_device_error().
- *   E            1 .. 256.  E * N must stay below 2^31.
+ *   E            1 .. 256.  E * N is at most 2^31 - 1025.
  * Every row's result is bit for bit gemm_int8_w8a8's of that row and expert. */
 NVFP4_API nvfp4_status gemm_int8_w8a8_grouped(const int8_t* A, const float* sA, const int8_t* W,
                                               const float* sW, const int32_t* offsets_dev, int E,
@@ -594,7 +594,7 @@ NVFP4_API nvfp4_status gemm_int8_w8a8_grouped(const int8_t* A, const float* sA, 
  * A row that holds an Inf or a NaN gets the scale NaN and zero codes (its products are
  * NaN; other rows are not touched).  X [rows][K] bf16 and codes [rows][K] int8 are
  * row-major and 16-byte aligned, scales [rows] float 4-byte aligned; K is a positive
- * multiple of 16, rows >= 0.  No workspace. */
+ * multiple of 16, rows 0 .. 2^31 - 1025.  No workspace. */
 NVFP4_API nvfp4_status int8_quantize_bf16(const void* X_bf16, int rows, int K, int8_t* codes,
                                           float* scales, void* stream);
 
@@ -631,7 +631,7 @@ NVFP4_API nvfp4_status int8_quantize_bf16_routed(const void* X_bf16, int rows, i
  *   ids        device int32 [T][k]; weights device float [T][k]
  *   E          1 .. 256; k 1 .. 32, at most top_groups * (E / groups)
  *   groups     1 .. 32, dividing E; 1 <= top_groups <= groups
- * logits are 16-byte aligned, the others 4-byte aligned.  No workspace; T >= 0. */
+ * logits are 16-byte aligned, the others 4-byte aligned.  No workspace; T 0 .. 2^31 - 1025. */
 typedef enum {
     NVFP4_SCORE_SOFTMAX = 0,
     NVFP4_SCORE_SIGMOID = 1

@@ -12,7 +12,7 @@ def test_argument_errors_need_no_device():
     def call(A=16, sA=4, W=16, sW=4, Y=16, M=4, N=4, K=64):
         return lib.gemm_int8_w8a8(A, sA, W, sW, Y, M, N, K, None)
     for kw in (dict(M=-1), dict(N=-1), dict(K=0), dict(K=8), dict(K=40), dict(K=-16),
-               dict(K=131072), dict(A=0), dict(sA=0), dict(W=0), dict(sW=0), dict(Y=0)):
+               dict(K=131072), dict(M=2 ** 31 - 1), dict(N=2 ** 31 - 1000), dict(A=0), dict(sA=0), dict(W=0), dict(sW=0), dict(Y=0)):
         assert call(**kw) == S.INVALID_ARG, kw
     for kw in (dict(A=24), dict(W=17), dict(Y=8), dict(sA=2), dict(sW=7)):
         assert call(**kw) == S.MISALIGNED, kw
@@ -24,7 +24,7 @@ def test_grouped_argument_errors_need_no_device():
     def call(A=16, off=4, E=2, M=4, N=4, K=64):
         return lib.gemm_int8_w8a8_grouped(A, 4, 16, 4, off, E, M, 16, N, K, None)
     for kw in (dict(E=0), dict(E=257), dict(E=-1), dict(off=0), dict(M=-1), dict(N=-2), dict(K=72),
-               dict(A=0), dict(E=256, N=2 ** 23)):
+               dict(A=0), dict(E=256, N=2 ** 23), dict(M=2 ** 31 - 1024)):
         assert call(**kw) == S.INVALID_ARG, kw
     assert call(off=6) == S.MISALIGNED
     assert call(A=40) == S.MISALIGNED
@@ -69,7 +69,7 @@ def test_quantiser_argument_errors_need_no_device():
 
     def call(X=16, rows=4, K=64, c=16, s=4):
         return lib.int8_quantize_bf16(X, rows, K, c, s, None)
-    for kw in (dict(rows=-1), dict(K=0), dict(K=8), dict(K=24), dict(X=0), dict(c=0), dict(s=0)):
+    for kw in (dict(rows=-1), dict(rows=2 ** 31 - 1), dict(K=0), dict(K=8), dict(K=24), dict(X=0), dict(c=0), dict(s=0)):
         assert call(**kw) == S.INVALID_ARG, kw
     for kw in (dict(X=18), dict(c=24), dict(s=6)):
         assert call(**kw) == S.MISALIGNED, kw
@@ -86,7 +86,7 @@ def test_router_argument_errors_need_no_device():
 
     def call(x=16, bf16=0, T=4, E=16, k=2, score=0, bias=4, groups=4, top=2, gt=2, ids=4, w=4):
         return lib.nvfp4_moe_topk(x, bf16, T, E, k, score, bias, groups, top, gt, 1, 1.0, ids, w, None)
-    for kw in (dict(T=-1), dict(E=0), dict(E=257), dict(k=0), dict(k=9), dict(k=33, E=256, groups=1, top=1),
+    for kw in (dict(T=-1), dict(T=2 ** 31 - 1), dict(E=0), dict(E=257), dict(k=0), dict(k=9), dict(k=33, E=256, groups=1, top=1),
                dict(score=2), dict(score=-1), dict(groups=3), dict(groups=0), dict(groups=64, E=128),
                dict(top=0), dict(top=5), dict(gt=0), dict(gt=3), dict(x=0), dict(ids=0), dict(w=0)):
         assert call(**kw) == S.INVALID_ARG, kw
