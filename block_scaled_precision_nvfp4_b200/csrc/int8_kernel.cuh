@@ -476,28 +476,41 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         uint8_t* const out = stages + (size_t)s.stages * sbytes + half * OUT_BYTES;
         const int g = lane >> 2, p2 = (lane & 3) * 2;  // fragment row, first of its two columns
         const bool wide = s.N % 8 == 0;                // 16-byte stores stay in a row
-        int tc = 0;
-        for (int t = cid; t < tiles; t += nclusters, ++tc) {
-            const Tile tl = decode(sm, s, t, nblk);
-            const int n0 = tl.n0 + (int)prank * BW;
-            float sw[4];  // channels g, g + 8, g + 16, g + 24 of the warp's 32
+        // What a tile needs beside its accumulator, fetched one tile ahead: the tile itself,
+        // the scales of channels g, g + 8, g + 16, g + 24 of the warp's 32, and on lane l the
+        // scale of token l of each of the warp's chunks.
+        struct Ahead {
+            Tile tl;
+            float sw[4], sa[MAX_BT / 64];
+        };
+        auto fetch = [&](int t) {
+            Ahead f;
+            f.tl = decode(sm, s, t, nblk);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int n = n0 + 32 * q + 8 * i + g;
-                sw[i] = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
+                const int n = f.tl.n0 + (int)prank * BW + 32 * q + 8 * i + g;
+                f.sw[i] = n < s.N ? __ldg(sW + (size_t)f.tl.e * s.N + n) : 0.f;
             }
-            // lane l: token l of each of the warp's chunks (in hand before the accumulator is)
-            float sa_lane[MAX_BT / 64];
 #pragma unroll
             for (int i = 0; i < MAX_BT / 64; ++i) {
                 const int j = half * 32 + i * 64 + lane;
-                sa_lane[i] = j < tl.rows ? __ldg(sA + tl.m0 + j) : 0.f;
+                f.sa[i] = j < f.tl.rows ? __ldg(sA + f.tl.m0 + j) : 0.f;
             }
+            return f;
+        };
+        int tc = 0;
+        Ahead next = {};
+        if (cid < tiles) next = fetch(cid);
+        for (int t = cid; t < tiles; t += nclusters, ++tc) {
+            const Ahead now = next;
+            const Tile tl = now.tl;
+            const int n0 = tl.n0 + (int)prank * BW;
             const int buf = tc & 1;
             // a warp that gives up here still meets its three others at the next barrier,
             // which tells all four
             bool ok = wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI);
             tc_fence_after();
+            if (t + nclusters < tiles) next = fetch(t + nclusters);
             const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
 #pragma unroll
             for (int cc = 0; cc < MAX_BT / 64; ++cc) {
@@ -511,7 +524,7 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 float sa[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    sa[i] = __shfl_sync(0xffffffffu, sa_lane[cc], 8 * (i >> 1) + p2 + (i & 1));
+                    sa[i] = __shfl_sync(0xffffffffu, now.sa[cc], 8 * (i >> 1) + p2 + (i & 1));
                 tmem_ld_wait();
                 reg_fence(r);
                 ok = named_bar_and(1 + half, 128, ok);  // the buffer's last chunk has left
@@ -522,8 +535,8 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int at = (k >> 1) * 16 + i * 4 + (k & 1) * 2;
-                        __nv_bfloat162 h = __floats2bfloat162_rn((float)(int)r[at] * (sw[k] * sa[2 * i]),
-                                                                 (float)(int)r[at + 1] * (sw[k] * sa[2 * i + 1]));
+                        __nv_bfloat162 h = __floats2bfloat162_rn((float)(int)r[at] * (now.sw[k] * sa[2 * i]),
+                                                                 (float)(int)r[at + 1] * (now.sw[k] * sa[2 * i + 1]));
                         m[k] = *reinterpret_cast<uint32_t*>(&h);
                     }
                     // lane l gives the address of row l & 7 (a token) of block l >> 3
