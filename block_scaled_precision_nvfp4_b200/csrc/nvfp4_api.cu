@@ -1398,6 +1398,7 @@ nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
 // pairs per tile, by the kernel's own measured costs (B200; M x 5376 x 14336):
 //   a 128-byte step of K   100 + 0.87 bt ns, at least 150   (64 tokens 156, 128 201, 256 322)
 //   the weights' bytes     6.2 TB/s
+//   a tile's epilogue      0.3 us + 8.5 ns per token column, under the next tile's steps
 //   a tile                 0.25 us (512 x 8 rows over 64 experts [2816, 2048], memory-bound:
 //                          65 us in tiles of 128 tokens, 69 in tiles of 64)
 //   a split tile           0.2 us + 55 ns per token for the exchange of sums
@@ -1428,12 +1429,13 @@ Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
                                            0.7 * std::max<double>(live, (double)M / c + 0.5 * live);
         for (int sp = 1; sp <= i8::MAX_SPLIT; ++sp) {
             if (sp > 1 && (bound * nblk > slots.clusters[sp] || steps < 2 * sp || c > i8::MAX_SPLIT_BT)) break;
-            const double per = (steps + sp - 1) / sp * std::max(0.150, 0.100 + 0.00087 * c);
+            const double epilogue = sp > 1 ? 0.0 : 0.3 + 0.0085 * c;  // under the next tile's steps
+            const double per = std::max((steps + sp - 1) / sp * std::max(0.150, 0.100 + 0.00087 * c), epilogue);
             const double w = blocks * nblk / slots.clusters[sp];
             // few waves end with a partly idle one; many even out (experts differ in size)
             const double waves = E == 1 || w < 2 ? std::ceil(w) : w + 0.5;
             const double compute = waves * per;
-            const double us = std::max(compute, mem_us) + 0.15 * compute + 0.25 * waves + 0.004 * c +
+            const double us = std::max(compute, mem_us) + 0.15 * compute + 0.25 * waves + epilogue +
                               0.008 * sp * std::min<double>(bound * nblk, slots.clusters[sp]) +
                               (sp > 1 ? 0.2 + 0.055 * std::min(c, M) : 0.0);
             if (us < best) {
