@@ -127,6 +127,17 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+// Two products rounded to nearest, in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 // Four 8 x 8 blocks of 16-bit values (fragment layout), each stored transposed: lane l
 // gives the address of row l % 8 of block l / 8.
 __device__ __forceinline__ void stmatrix_x4_trans(void* row, const uint32_t (&m)[4]) {
@@ -521,10 +532,11 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                     tmem_ld_16x256b_x4(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
                     tmem_ld_16x256b_x4(acc + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
                 }
-                float sa[8];
+                float2 sa[4];  // the two tokens of each 8
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sa[i] = __shfl_sync(0xffffffffu, now.sa[cc], 8 * (i >> 1) + p2 + (i & 1));
+                for (int i = 0; i < 4; ++i)
+                    sa[i] = make_float2(__shfl_sync(0xffffffffu, now.sa[cc], 8 * i + p2),
+                                        __shfl_sync(0xffffffffu, now.sa[cc], 8 * i + p2 + 1));
                 tmem_ld_wait();
                 reg_fence(r);
                 ok = named_bar_and(1 + half, 128, ok);  // the buffer's last chunk has left
@@ -535,8 +547,9 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int at = (k >> 1) * 16 + i * 4 + (k & 1) * 2;
-                        __nv_bfloat162 h = __floats2bfloat162_rn((float)(int)r[at] * (now.sw[k] * sa[2 * i]),
-                                                                 (float)(int)r[at + 1] * (now.sw[k] * sa[2 * i + 1]));
+                        const float2 f = mul2(make_float2(now.sw[k], now.sw[k]), sa[i]);
+                        const float2 v = mul2(make_float2((float)(int)r[at], (float)(int)r[at + 1]), f);
+                        __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
                         m[k] = *reinterpret_cast<uint32_t*>(&h);
                     }
                     // lane l gives the address of row l & 7 (a token) of block l >> 3

@@ -1401,7 +1401,7 @@ nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
 //   a tile's epilogue      0.3 us + 8.5 ns per token column, under the next tile's steps
 //   a tile                 0.25 us (512 x 8 rows over 64 experts [2816, 2048], memory-bound:
 //                          65 us in tiles of 128 tokens, 69 in tiles of 64)
-//   a split tile           0.2 us + 55 ns per token for the exchange of sums
+//   a split tile           0.5 us + 55 ns per token for the exchange of sums
 //                          (64 tokens: 18 us on 3 pairs a tile, 21.5 unsplit)
 //   a pair that takes part 8 ns
 // A split is taken only where all of its clusters run at once: with several split tiles
@@ -1437,7 +1437,7 @@ Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
             const double compute = waves * per;
             const double us = std::max(compute, mem_us) + 0.15 * compute + 0.25 * waves + epilogue +
                               0.008 * sp * std::min<double>(bound * nblk, slots.clusters[sp]) +
-                              (sp > 1 ? 0.2 + 0.055 * std::min(c, M) : 0.0);
+                              (sp > 1 ? 0.5 + 0.055 * std::min(c, M) : 0.0);
             if (us < best) {
                 best = us;
                 bt = c;

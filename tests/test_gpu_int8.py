@@ -90,6 +90,16 @@ def test_a_nan_or_inf_scale_stays_in_its_row_and_channel():
         assert nan.sum() == M + 140 - 1
 
 
+def test_operands_may_be_one_buffer_and_scales_start_anywhere():
+    """A . A^T, and scales that are slices (4-byte aligned)."""
+    rng = np.random.default_rng(12)
+    A, s = _codes(rng, 150, 400), _scales(rng, 153)
+    dA, ds = _d(A), _d(s)
+    for o in (1, 2, 3):
+        y = nv.gemm_int8_w8a8(dA, ds[o:150 + o], dA, ds[3 - o:153 - o])
+        _close(y, _ref(A, s[o:150 + o], A, s[3 - o:153 - o]))
+
+
 def test_rows_do_not_depend_on_their_batch():
     """One row alone, in a small batch and in a large one: the same bits (split K, single
     SMs and pairs of SMs all sum the same integers and scale in the same order)."""

@@ -257,3 +257,36 @@ def test_int8_expert_layer(T, k, E, N, K, kw):
     torch.cuda.synchronize()
     for a, b in zip(captured, again):
         assert torch.equal(a, b)
+
+
+def test_nvfp4_expert_layer_from_the_routers_logits():
+    """The same routing ahead of the NVFP4 experts: planned, packed and multiplied from device
+    offsets, combined with the router's weights -- bit for bit the layer that gets the
+    formula's ids and weights from the host."""
+    from block_scaled_precision_nvfp4_b200 import workloads as wl
+    rng = np.random.default_rng(31)
+    T, k, E, N, K = 333, 2, 8, 512, 512
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(torch.bfloat16).cuda()
+    experts = [wl.quantize_nvfp4(rng.standard_normal((N, K), dtype=np.float32) * np.float32(0.02))
+               for _ in range(E)]
+    W = torch.from_numpy(np.stack([e.codes for e in experts])).cuda()
+    sW = torch.from_numpy(np.stack([e.scales for e in experts])).cuda()
+    sw_p = nv.nvfp4_pack_scales_grouped(sW.view(E * N, K // 16), [i * N for i in range(E + 1)], K)
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    bias = torch.from_numpy(0.1 * rng.standard_normal(E).astype(np.float32)).cuda()
+
+    def layer(ids, weights):
+        off, dest, src = nv.moe_route(ids, E)
+        codes, scales, g = nv.nvfp4_quantize_bf16_routed(x, dest, k)
+        sched = nv.GroupedSchedule(off, E, T * k, N, K, [e.g for e in experts], gA=g)
+        y = sched.gemm(codes, sched.pack(scales), W, sw_p)
+        return nv.moe_combine(y, dest, weights, T, k)
+    ids, weights = nv.moe_topk(logits, k, score="sigmoid", bias=bias)
+    Y = layer(ids, weights)
+    ri, rw = _oracle(logits.cpu().numpy(), k, score="sigmoid", bias=bias.cpu().numpy())
+    assert np.array_equal(ids.cpu().numpy(), ri)
+    assert (np.abs(weights.cpu().numpy() - rw) <= 2.0 ** -23 * rw).all()
+    ref = layer(torch.from_numpy(ri).cuda(), weights)
+    torch.cuda.synchronize()
+    nv.nvfp4_check_device_error()
+    assert torch.equal(Y.view(torch.int16), ref.view(torch.int16)) and Y.float().abs().max() > 0
