@@ -182,11 +182,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 //   sigmoid: exp moves s by at most 1.6 (s (1 - s) <= 1/4 and s (1 - s) |x| <= 0.23);
 //     1 + exp adds 1, the fast division 4: 6.6 in all.
 //   softmax: exp is off by 2 + d relative at d = max - x (its argument's rounding), at
-//     most 2.4 of s <= 1 (s d <= 0.37); the sum by 29 (the same, d weighted by the terms
-//     at most ln 256, and 21 additions); the division and the product add 2: 34 in all.
+//     most 2.4 of s <= 1 (s d <= 0.37); the sum by 9 (the same, d weighted by the terms
+//     at most ln 256, and its rounding); the division and the product add 2: 14 in all.
 //   the bias' addition: |c|.
 __device__ __forceinline__ float gap(float mag, bool sigmoid) {
-    return (sigmoid ? 16.0f : 74.0f) * 0x1p-24f + fabsf(mag) * 0x1p-22f;
+    return (sigmoid ? 16.0f : 32.0f) * 0x1p-24f + fabsf(mag) * 0x1p-22f;
 }
 
 template <int V, typename X>
@@ -235,7 +235,8 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
 
     float c[V];  // what the experts are ordered by: the choices, or without a bias the logits
     load_logits<V, X>(row, e0, cnt, p.vec != 0, c);
-    float xmax = 0.f, sum = 0.f;
+    float xmax = 0.f;
+    double sum = 0.0;  // of FP32 exponentials: their errors average out, additions would not
     if (!p.sigmoid) {
         uint32_t m = 0;
 #pragma unroll
@@ -253,11 +254,11 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 s[v] = c[v] > -INFINITY ? expf(c[v] - xmax) : 0.f;
-                sum += s[v];
+                sum += (double)s[v];
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-            const float inv = sum > 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+            const float inv = sum > 0.0 ? __fdiv_rn(1.0f, (float)sum) : 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] *= inv;
         }
@@ -439,7 +440,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         x = (double)f;
         sc = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : f > -INFINITY ? exp(x - (double)xmax) : 0.0;
     }
-    double sum64 = (double)sum;
+    double sum64 = sum;
     if (near && !p.sigmoid) {  // the softmax's sum in 64 bits too
         float f[V];
         load_logits<V, X>(row, e0, cnt, p.vec != 0, f);
