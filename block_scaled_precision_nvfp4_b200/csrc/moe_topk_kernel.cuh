@@ -50,7 +50,6 @@ struct Params {
     float scale;
     int per, lpg;    // experts of a group, lanes of a group
     int lanes;       // lanes that hold at least one expert of the kept groups
-    int vec;         // every lane's run of logits starts on a 16-byte (BF16: 8-byte) boundary
 };
 
 constexpr float FLT_LARGEST = 3.402823466e38f;
@@ -192,7 +191,7 @@ __device__ __forceinline__ float gap(float mag, bool sigmoid) {
 template <int V, typename X>
 __device__ __forceinline__ void load_logits(const X* __restrict__ row, int e0, int cnt, bool vec,
                                             float (&x)[V]) {
-    if (vec && cnt == V) {
+    if (vec) {
         if constexpr (sizeof(X) == 4 && V % 4 == 0) {
 #pragma unroll
             for (int v = 0; v < V; v += 4) {
@@ -216,7 +215,8 @@ __device__ __forceinline__ void load_logits(const X* __restrict__ row, int e0, i
     for (int v = 0; v < V; ++v) x[v] = fminf(fmaxf(x[v], -INFINITY), FLT_LARGEST);
 }
 
-template <int V, typename X>
+// FULL_LANES: every lane holds exactly V experts, on 16-byte (BF16: 8-byte) boundaries.
+template <int V, typename X, bool FULL_LANES>
 __global__ void __launch_bounds__(32 * WARPS, V <= 8 ? 8 : 4)
 moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
                 int32_t* __restrict__ ids, float* __restrict__ weights,
@@ -229,12 +229,12 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
     if (t >= p.T) return;
     const int g = lane / p.lpg, i0 = (lane % p.lpg) * V;
     const int e0 = g * p.per + i0;
-    const int cnt = g < p.groups ? max(0, min(V, p.per - i0)) : 0;
+    const int cnt = FULL_LANES ? V : g < p.groups ? max(0, min(V, p.per - i0)) : 0;
     const X* const row = logits + (size_t)t * p.E;
     const bool group_sum = p.groups > 1 && p.group_top == 2 && p.per > 1;
 
     float c[V];  // what the experts are ordered by: the choices, or without a bias the logits
-    load_logits<V, X>(row, e0, cnt, p.vec != 0, c);
+    load_logits<V, X>(row, e0, cnt, FULL_LANES, c);
     float xmax = 0.f;
     double sum = 0.0;  // of FP32 exponentials: their errors average out, additions would not
     if (!p.sigmoid) {
@@ -264,14 +264,22 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
         }
     }
     if (bias) {
+        float b[V];
+        if constexpr (FULL_LANES) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float b = v < cnt ? __ldg(bias + e0 + v) : 0.f;
-            c[v] = fmaxf(s[v] + b, -INFINITY);  // a NaN counts as -Inf
+            for (int v = 0; v < V; v += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(bias + e0 + v));
+                b[v] = f.x, b[v + 1] = f.y, b[v + 2] = f.z, b[v + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) b[v] = v < cnt ? __ldg(bias + e0 + v) : 0.f;
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = fmaxf(s[v] + b[v], -INFINITY);  // a NaN counts as -Inf
     }
 
-    bool kept = g < p.groups;
+    bool kept = FULL_LANES || g < p.groups;
     if (p.groups > 1) {
         float a = -INFINITY, b = -INFINITY;
 #pragma unroll
@@ -443,7 +451,7 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
     double sum64 = sum;
     if (near && !p.sigmoid) {  // the softmax's sum in 64 bits too
         float f[V];
-        load_logits<V, X>(row, e0, cnt, p.vec != 0, f);
+        load_logits<V, X>(row, e0, cnt, FULL_LANES, f);
         sum64 = 0.0;
 #pragma unroll 1
         for (int v = 0; v < V; ++v) {

@@ -293,13 +293,15 @@ cudaError_t launch_programmatic(void (*kern)(P...), dim3 grid, int threads, void
 }
 
 template <typename X>
-void (*topk_kernel_for(int v))(const X*, const float*, int32_t*, float*, nvfp4::topk::Params) {
+void (*topk_kernel_for(int slots, bool full))(const X*, const float*, int32_t*, float*, nvfp4::topk::Params) {
     namespace tk = nvfp4::topk;
-    if (v <= 1) return tk::moe_topk_kernel<1, X>;
-    if (v <= 2) return tk::moe_topk_kernel<2, X>;
-    if (v <= 4) return tk::moe_topk_kernel<4, X>;
-    if (v <= 8) return tk::moe_topk_kernel<8, X>;
-    return tk::moe_topk_kernel<16, X>;
+    switch (slots) {
+        case 1: return tk::moe_topk_kernel<1, X, false>;
+        case 2: return tk::moe_topk_kernel<2, X, false>;
+        case 4: return full ? tk::moe_topk_kernel<4, X, true> : tk::moe_topk_kernel<4, X, false>;
+        case 8: return full ? tk::moe_topk_kernel<8, X, true> : tk::moe_topk_kernel<8, X, false>;
+        default: return tk::moe_topk_kernel<16, X, false>;
+    }
 }
 
 }  // namespace
@@ -1622,19 +1624,21 @@ nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, i
         return fail(NVFP4_ERR_NOPATH, "the router is compiled for sm_100 only (device sm_%d)", info.sm_arch);
     if (T == 0) return ok();
     tk::Params p = {T, E, k, score == NVFP4_SCORE_SIGMOID, groups, top_groups, group_top,
-                    renormalize != 0, scale, per, 32, 0, 0};
+                    renormalize != 0, scale, per, 32, 0};
     while (p.lpg * groups > 32) p.lpg /= 2;  // a power of two of lanes for each group
     const int v = (per + p.lpg - 1) / p.lpg;
     const int slots = v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : v <= 8 ? 8 : 16;  // experts of a lane
     p.lanes = top_groups * ((per + slots - 1) / slots);
-    p.vec = v > 2 && E % 4 == 0 && per % 4 == 0;  // runs of 4 or more
+    // every lane full and aligned (32, 64, .. 256 experts in 1, 2, .. groups): no lane checks
+    // its count, and logits and bias come in 16-byte pieces
+    const bool full = per == slots * p.lpg && groups * p.lpg == 32 && reinterpret_cast<uintptr_t>(bias) % 16 == 0;
     const dim3 grid((unsigned)((T + tk::WARPS - 1) / tk::WARPS));
     cudaError_t e;
     if (logits_bf16)
-        e = launch_programmatic(topk_kernel_for<__nv_bfloat16>(v), grid, 32 * tk::WARPS, stream,
+        e = launch_programmatic(topk_kernel_for<__nv_bfloat16>(slots, full), grid, 32 * tk::WARPS, stream,
                                 static_cast<const __nv_bfloat16*>(logits), bias, ids, weights, p);
     else
-        e = launch_programmatic(topk_kernel_for<float>(v), grid, 32 * tk::WARPS, stream,
+        e = launch_programmatic(topk_kernel_for<float>(slots, full), grid, 32 * tk::WARPS, stream,
                                 static_cast<const float*>(logits), bias, ids, weights, p);
     if (e != cudaSuccess) return cuda_fail(e, "launching moe_topk_kernel");
     return ok();
