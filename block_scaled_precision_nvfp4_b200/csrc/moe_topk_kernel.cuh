@@ -17,16 +17,18 @@
 // compared as they are.  Otherwise the choices are computed in FP32 with a proven error
 // bound; the list of the best is extended until nothing outside it can belong to the first
 // k, and where two neighbours are closer than the bound allows, it is ranked again by
-// 64-bit choices, one list entry per lane.  What that cannot settle (groups closer than
-// the bound, more near-ties than lanes) goes through the whole token in 64 bits.  Weights are always 64-bit values of the k chosen scores, rounded once.
+// 64-bit choices, one list entry per lane.  Groups closer than the bound are chosen by
+// 64-bit sums; a token with more near-ties than lanes goes through 64 bits as a whole.
+// Weights are always 64-bit values of the k chosen scores, rounded once.
 //
 // One warp per token; a group's experts sit on `lpg` neighbouring lanes, V per lane, in
 // ascending order, so the lowest lane and the lowest slot hold the lowest index.  Few
 // bytes, many instructions: bound by the integer and compare pipe (80 % of its rate).
-// 8192 tokens over 256 experts in 8 groups (8.9 MB, 1.4 us of HBM) take 12.0 us, 65536 of
-// them 74 us; everything in 64 bits took 28.8 us, selection rounds over all of a lane's
-// experts instead of the packed list 14.8 us (but for up to 2 experts per lane they are the
-// faster form: 64 experts 5.5 against 6.0 us).
+// 8192 tokens over 256 experts in 8 groups (8.9 MB, 1.4 us of HBM) take 9.7 us, 65536 of
+// them 66 us.  Everything in 64 bits took 28.8 us; selection rounds over all of a lane's
+// experts instead of the packed list 14.8 against 12.0 us (but for up to 2 experts per lane
+// they are the faster form: 64 experts 5.5 against 6.0 us); a whole token in 64 bits where
+// only its groups are too close, 11.7 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -54,11 +56,12 @@ struct Params {
 
 constexpr float FLT_LARGEST = 3.402823466e38f;
 
-// One token by the formulas in 64 bits, by its whole warp.
+// One token's logits x, scores s and choices c by the formulas in 64 bits, by its whole
+// warp; returns whether the lane's group is kept.
 template <int V, typename X>
-__device__ __noinline__ void topk_exact(const X* __restrict__ logits, const float* __restrict__ bias,
-                                        int32_t* __restrict__ ids, float* __restrict__ weights,
-                                        const Params& p, int t) {
+__device__ __forceinline__ bool exact_choices(const X* __restrict__ logits, const float* __restrict__ bias,
+                                              const Params& p, int t, double (&x)[V], double (&s)[V],
+                                              double (&c)[V]) {
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     const double NEG = -__longlong_as_double(0x7FF0000000000000ll);
@@ -66,7 +69,6 @@ __device__ __noinline__ void topk_exact(const X* __restrict__ logits, const floa
     const int e0 = g * p.per + i0;
     const int cnt = g < p.groups ? max(0, min(V, p.per - i0)) : 0;
 
-    double x[V], s[V], c[V];  // logits, scores, choices
     double xmax = NEG;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -125,6 +127,30 @@ __device__ __noinline__ void topk_exact(const X* __restrict__ logits, const floa
         }
         kept = kept && better < p.top_groups;
     }
+    return kept;
+}
+
+// Whether the lane's group is kept, where FP32 sums are too close to tell.
+template <int V, typename X>
+__device__ __noinline__ bool group_kept_exact(const X* __restrict__ logits, const float* __restrict__ bias,
+                                              const Params& p, int t) {
+    double x[V], s[V], c[V];
+    return exact_choices<V, X>(logits, bias, p, t, x, s, c);
+}
+
+// The whole token in 64 bits.
+template <int V, typename X>
+__device__ __noinline__ void topk_exact(const X* __restrict__ logits, const float* __restrict__ bias,
+                                        int32_t* __restrict__ ids, float* __restrict__ weights,
+                                        const Params& p, int t) {
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const double NEG = -__longlong_as_double(0x7FF0000000000000ll);
+    const int g = lane / p.lpg, i0 = (lane % p.lpg) * V;
+    const int e0 = g * p.per + i0;
+    const int cnt = g < p.groups ? max(0, min(V, p.per - i0)) : 0;
+    double x[V], s[V], c[V];
+    const bool kept = exact_choices<V, X>(logits, bias, p, t, x, s, c);
 
     // k rounds: the best expert left, by (choice, lowest index)
     unsigned left = kept ? (1u << cnt) - 1u : 0u;
@@ -215,7 +241,8 @@ __device__ __forceinline__ void load_logits(const X* __restrict__ row, int e0, i
     for (int v = 0; v < V; ++v) x[v] = fminf(fmaxf(x[v], -INFINITY), FLT_LARGEST);
 }
 
-// FULL_LANES: every lane holds exactly V experts, on 16-byte (BF16: 8-byte) boundaries.
+// FULL_LANES: every lane holds exactly V experts, on 16-byte (BF16: 8-byte) boundaries
+// (65536 x 256 in 8 groups: 68 us, 72 without).
 template <int V, typename X, bool FULL_LANES>
 __global__ void __launch_bounds__(32 * WARPS, V <= 8 ? 8 : 4)
 moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
@@ -309,10 +336,8 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
             // the terms of the largest finite sum bound every sum's error (infinite ones are exact)
             const float mag = key_value(__reduce_max_sync(
                 FULL, order_key(exists && fabsf(gs) < INFINITY ? fabsf(a) + (group_sum ? fabsf(b) : 0.f) : 0.f)));
-            if (lo - hi <= 2.0f * gap(mag, p.sigmoid != 0)) {  // false for two equal infinities
-                topk_exact<V, X>(logits, bias, ids, weights, p, t);
-                return;
-            }
+            if (lo - hi <= 2.0f * gap(mag, p.sigmoid != 0))  // false for two equal infinities
+                kept = group_kept_exact<V, X>(logits, bias, p, t);
         }
     }
 
