@@ -27,7 +27,8 @@
 // bt for the tokens, against 2 bt clocks of MMA: tiles of 256 tokens are the smallest that
 // the MMA bounds.  Measured per step: 156 ns at 64 tokens, 201 at 128, 322 at 256 with
 // every SM busy.  Large products are bound by power: 4096 x 5376 x 14336 takes 163 us on
-// zeros and 199 us on random codes.  Small ones by the weights' bytes (6.2 TB/s reached).
+// zeros and 199 us on random codes.  Small ones by the weights' bytes (32 rows over 8
+// experts [14336, 4096]: 72 us, 6.5 TB/s; one token at 5376 x 14336: 15.1 us, 5.1 TB/s).
 // Single SMs instead of pairs (M = 128) took 31 us for 333 tokens where pairs take 27, and
 // 78 us for 32 tokens over 8 experts where pairs take 75.
 #pragma once
@@ -77,8 +78,7 @@ struct Smem {
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint64_t drain;
-    uint64_t red_full;  // split tiles: every source's partial sums of the tile are here
-    uint64_t red_free;  // split tiles: every owner has read this CTA's partial sums
+    uint64_t red_full;  // split tile: every source's partial sums are here
     uint32_t tmem_base;
     int abort;
     int bad;
@@ -183,12 +183,6 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
         : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
-// Arrive on `bar`'s counterpart in CTA `rank`, releasing at cluster scope.
-__device__ __forceinline__ void arrive_release_cluster(uint64_t* bar, uint32_t rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                 ::"r"(map_to_rank(bar, rank)) : "memory");
-}
-
 // Bounded wait of a whole converged warp (mbar_wait's limit and error record).  Every lane
 // polls, so no shuffle or branch stands between the barrier and the work behind it, and
 // the clock and the abort flag are looked at once every 32 polls: a K-block of one tile of
@@ -355,7 +349,6 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
         }
         mbar_init(&sm.drain, 1);
         mbar_init(&sm.red_full, 1);
-        mbar_init(&sm.red_free, s.split * NUM_EPI_WARPS);
         sm.abort = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmW);
@@ -454,8 +447,8 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
 #pragma unroll
                             for (int ks = 0; ks < KSTEPS; ++ks)
                                 mma_i8(acc, w_desc0 + (step + c * (BW * BKB / 16) + ks * 2),
-                                             a_desc0 + (step + c * (tokbytes >> 4) + ks * 2), idesc,
-                                             kb != kb0 || c != 0 || ks != 0);
+                                       a_desc0 + (step + c * (tokbytes >> 4) + ks * 2), idesc,
+                                       kb != kb0 || c != 0 || ks != 0);
                         mma_commit_pair(&sm.empty[st], 0x3 << lead);
                     }
                     __syncwarp();
@@ -611,31 +604,27 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             // one that the MMA warp waits for, so none can reach a CTA that has left)
             if (lane == 0 && t + 2 * nclusters < tiles) mbar_arrive_remote(&sm.acc_empty[buf], lead);
         }
-    } else {
-        // ------------------------------------------------------------ epilogue, split tiles
-        // Each CTA sends its INT32 partial sums to the columns' owners, as [source][column
+    } else if (cid < tiles) {
+        // ------------------------------------------------------------ epilogue, a split tile
+        // (one per cluster: the host splits only where all tiles run at once.)  Each CTA
+        // sends its INT32 partial sums to the columns' owners, as [source][column
         // quad][channel] int4; an owner adds its columns' sums and stores them.
         const int q = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
         const int tid = threadIdx.x - 32 * FIRST_EPI_WARP, ch = tid & (BW - 1);
         uint8_t* const red = stages + (size_t)s.stages * sbytes;
-        int tc = 0;
-        for (int t = cid; t < tiles; t += nclusters, ++tc) {
-            const Tile tl = decode(sm, s, t, nblk);
-            const int cw = share_cols(tl.rows, s.split), quads = cw / 4;
-            const int my_cols = max(0, min(cw, tl.rows - part * cw));
-            const int n = tl.n0 + (int)prank * BW + ch;
-            const float sw = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
-            // lane l: the scales of this pair's tokens l and 32 + l (a share is at most 64)
-            const int m0 = tl.m0 + part * cw;
-            const float sa0 = lane < my_cols ? __ldg(sA + m0 + lane) : 0.f;
-            const float sa1 = 32 + lane < my_cols ? __ldg(sA + m0 + 32 + lane) : 0.f;
-            if (tid == 0) mbar_arrive_expect_tx(&sm.red_full, s.split * ((my_cols + 3) / 4) * BW * 16);
-            const int buf = tc & 1;
-            if (!wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI)) break;
-            // the owners have read this CTA's sums of the tile before
-            if (tc > 0 && !wait_bar<true>(&sm.red_free, (tc - 1) & 1, abort, ROLE_EPI)) break;
+        const Tile tl = decode(sm, s, cid, nblk);
+        const int cw = share_cols(tl.rows, s.split), quads = cw / 4;
+        const int my_cols = max(0, min(cw, tl.rows - part * cw));
+        const int n = tl.n0 + (int)prank * BW + ch;
+        const float sw = n < s.N ? __ldg(sW + (size_t)tl.e * s.N + n) : 0.f;
+        // lane l: the scales of this pair's tokens l and 32 + l (a share is at most 64)
+        const int m0 = tl.m0 + part * cw;
+        const float sa0 = lane < my_cols ? __ldg(sA + m0 + lane) : 0.f;
+        const float sa1 = 32 + lane < my_cols ? __ldg(sA + m0 + 32 + lane) : 0.f;
+        if (tid == 0) mbar_arrive_expect_tx(&sm.red_full, s.split * ((my_cols + 3) / 4) * BW * 16);
+        if (wait_bar(&sm.acc_full[0], 0, abort, ROLE_EPI)) {
             tc_fence_after();
-            const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
             const uint32_t src = smem_u32(red) + (uint32_t)(part * quads * BW + 32 * q + lane) * 16;
             for (int c = half * 32; c < tl.rows; c += 64) {
                 uint32_t r[32];
@@ -657,11 +646,8 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                 }
             }
             tc_fence_before();
-            __syncwarp();
-            // (a buffer that no later tile takes is not handed back: every remote arrive is
-            // one that the MMA warp waits for, so none can reach a CTA that has left)
-            if (lane == 0 && t + 2 * nclusters < tiles) mbar_arrive_remote(&sm.acc_empty[buf], lead);
-            if (!wait_bar<true>(&sm.red_full, tc & 1, abort, ROLE_EPI)) break;
+        }
+        if (wait_bar<true>(&sm.red_full, 0, abort, ROLE_EPI)) {
             for (int c = tid / BW; c * 4 < my_cols; c += NUM_EPI_WARPS * 32 / BW) {
                 int4 v = make_int4(0, 0, 0, 0);
                 for (int i = 0; i < s.split; ++i) {
@@ -680,9 +666,6 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                         Y[(size_t)(m0 + col) * s.N + n] = __float2bfloat16_rn((float)sum[j] * (sw * sa));
                 }
             }
-            __syncwarp();
-            if (t + nclusters < tiles && lane < s.split)
-                arrive_release_cluster(&sm.red_free, (uint32_t)lane * CTAS + prank);
         }
     }
 

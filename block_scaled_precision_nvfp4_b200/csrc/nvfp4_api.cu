@@ -1406,8 +1406,9 @@ nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
 //   a split tile           0.5 us + 55 ns per token for the exchange of sums
 //                          (64 tokens: 18 us on 3 pairs a tile, 21.5 unsplit)
 //   a pair that takes part 8 ns
-// A split is taken only where all of its clusters run at once: with several split tiles
-// per cluster the exchange is not hidden (333 tokens: 43 us on 3 pairs a tile, 27 unsplit).
+// A split is taken only where all of its clusters run at once, one tile each: with several
+// split tiles per cluster the exchange is not hidden (333 tokens: 43 us on 3 pairs a tile,
+// 27 unsplit).  Two steps of K per pair at least, so that each has a stage to multiply.
 Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
     namespace i8 = nvfp4::int8;
     const int steps = (K + i8::BKB - 1) / i8::BKB;
