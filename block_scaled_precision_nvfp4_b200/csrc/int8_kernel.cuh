@@ -424,7 +424,7 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
 #ifdef NVFP4_WAIT_TEST
             // test-only: wait for a commit that has not been issued, so that this bounded
             // wait expires and every role of the cluster takes its abort path
-            if (g_wait_test_stall && !wait_bar(&sm.drain, 0, abort, ROLE_MMA)) ok = false;
+            if (g_wait_test_stall == 1 && !wait_bar(&sm.drain, 0, abort, ROLE_MMA)) ok = false;
 #endif
             // descriptors of stage 0; a stage further is sbytes / 16 more in the address field
             const uint64_t w_desc0 = desc_kmajor_sw128(smem_u32(stages));
@@ -510,9 +510,17 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             const Tile tl = now.tl;
             const int n0 = tl.n0 + (int)prank * BW;
             const int buf = tc & 1;
-            // a warp that gives up here still meets its three others at the next barrier,
-            // which tells all four
+            // A warp that gives up here still meets its three others at the tile's first
+            // barrier, which tells all four.  Every tile has one in either half, so none of
+            // them goes on to a tile that the others will not come to.
             bool ok = wait_bar(&sm.acc_full[buf], (tc >> 1) & 1, abort, ROLE_EPI);
+#ifdef NVFP4_WAIT_TEST
+            // test-only: one warp's wait counts as expired although the others' did not
+            if (g_wait_test_stall == 2 && tc == 0 && warp == FIRST_EPI_WARP + 4) {
+                if (lane == 0) atomicOr(&g_device_error, 1 | (ROLE_EPI << 8));
+                ok = false;
+            }
+#endif
             tc_fence_after();
             if (t + nclusters < tiles) next = fetch(t + nclusters);
             const uint32_t acc = tmem + buf * acc_stride + ((uint32_t)(32 * q) << 16);
@@ -597,6 +605,7 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                     }
                 }
             }
+            if (half * 32 >= tl.rows) ok = named_bar_and(1 + half, 128, ok);  // no chunk, no barrier yet
             if (!ok) break;
             tc_fence_before();
             __syncwarp();

@@ -1678,13 +1678,36 @@ nvfp4_status nvfp4_prepare_scales(const uint8_t* s_plain, uint8_t* s_mma, int ro
 }
 
 #ifdef NVFP4_WAIT_TEST
-// Test-only build: sets the pipeline waits' time limit and the stall switch of
-// the single-SM W4A4 kernel on the current device.  Not in the product library.
+// Test-only build: sets the pipeline waits' time limit and the stall switch (0 none, 1 the
+// MMA role of the single-SM W4A4 and the INT8 kernel, 2 one epilogue warp of the INT8
+// kernel) on the current device.  Not in the product library.
 __attribute__((visibility("default"))) nvfp4_status nvfp4_test_set_wait(uint64_t limit_ns,
                                                                         int stall) {
     cudaError_t e = cudaMemcpyToSymbol(nvfp4::g_wait_limit_ns, &limit_ns, sizeof(limit_ns));
     if (e == cudaSuccess) e = cudaMemcpyToSymbol(nvfp4::g_wait_test_stall, &stall, sizeof(stall));
     return e == cudaSuccess ? ok() : cuda_fail(e, "setting the test wait variables");
+}
+
+// The INT8 products' plan for sizes (host only): clusters[i] are the clusters of i pairs (1..4)
+// that run at once; with use_device they are the current device's, and returned there.  out = token columns, pairs per tile, chunks, stages, tiles, CTAs.
+__attribute__((visibility("default"))) nvfp4_status nvfp4_test_int8_plan(int M, int N, int K, int E,
+                                                                         int use_device, int* clusters,
+                                                                         int* out) {
+    Int8Slots slots;
+    if (use_device) {
+        int dev;
+        DevInfo info;
+        if (!current_device(dev, info)) return fail(NVFP4_ERR_CUDA, "cannot query the current CUDA device");
+        const nvfp4_status st = int8_slots(dev, info, slots);
+        if (st != NVFP4_OK) return st;
+        for (int i = 0; i <= nvfp4::int8::MAX_SPLIT; ++i) clusters[i] = slots.clusters[i];
+    } else {
+        for (int i = 0; i <= nvfp4::int8::MAX_SPLIT; ++i) slots.clusters[i] = clusters[i];
+    }
+    const Int8Plan p = int8_plan(M, N, K, E, slots);
+    const int v[6] = {p.shape.bt, p.shape.split, p.shape.chunks, p.shape.stages, (int)p.tiles, p.grid};
+    std::copy(v, v + 6, out);
+    return ok();
 }
 #endif
 
