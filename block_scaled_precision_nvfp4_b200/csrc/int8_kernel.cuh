@@ -656,7 +656,14 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
             }
             tc_fence_before();
         }
-        if (wait_bar<true>(&sm.red_full, 0, abort, ROLE_EPI)) {
+#ifdef NVFP4_WAIT_TEST
+        // test-only: the owners' waits count as expired, with sums still on their way to them
+        const bool expired = g_wait_test_stall == 3 && my_cols > 0;
+        if (expired && tid == 0) atomicOr(&g_device_error, 1 | (ROLE_EPI << 8));
+#else
+        constexpr bool expired = false;
+#endif
+        if (!expired && wait_bar<true>(&sm.red_full, 0, abort, ROLE_EPI)) {
             for (int c = tid / BW; c * 4 < my_cols; c += NUM_EPI_WARPS * 32 / BW) {
                 int4 v = make_int4(0, 0, 0, 0);
                 for (int i = 0; i < s.split; ++i) {
@@ -685,6 +692,14 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
     cluster_arrive_relaxed();
     cluster_wait();
     tc_fence_after();
+    // By now every partial sum of a split tile has been sent, but a CTA whose wait for them
+    // expired may still be their target: it stays until they have landed (or until the limit,
+    // when some were never sent).  Otherwise this is one look at a completed barrier.
+    if (s.split > 1 && warp == 0 && cid < tiles) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!try_wait_cluster(&sm.red_full, 0) && globaltimer_ns() - t0 < wait_limit_ns()) {
+        }
+    }
     if (warp == 1) tmem_dealloc_pair(tmem, tmem_cols(s.bt));
 }
 

@@ -1680,7 +1680,7 @@ nvfp4_status nvfp4_prepare_scales(const uint8_t* s_plain, uint8_t* s_mma, int ro
 #ifdef NVFP4_WAIT_TEST
 // Test-only build: sets the pipeline waits' time limit and the stall switch (0 none, 1 the
 // MMA role of the single-SM W4A4 and the INT8 kernel, 2 one epilogue warp of the INT8
-// kernel) on the current device.  Not in the product library.
+// kernel's whole tiles, 3 the receivers of its split tiles) on the current device.  Not in the product library.
 __attribute__((visibility("default"))) nvfp4_status nvfp4_test_set_wait(uint64_t limit_ns,
                                                                         int stall) {
     cudaError_t e = cudaMemcpyToSymbol(nvfp4::g_wait_limit_ns, &limit_ns, sizeof(limit_ns));
