@@ -4,8 +4,11 @@
 //
 // a, w are signed 8-bit codes, sA one FP32 scale per token (row of A), sW one per
 // output channel (row of W).  The sum over k is an exact INT32 sum (K <= 131056, so
-// that even codes of -128 cannot overflow it); the two scales are applied in FP32 and
-// the result is rounded once to BF16.
+// that even codes of -128 cannot overflow it); in FP32 it is multiplied by sW, then by sA,
+// and the result is rounded once to BF16.  (Not by sW * sA: that product can leave FP32's
+// range where the result does not.  A sum other than 0 times an sW of 2^-126 .. 2^96 is
+// normal, and is then rounded where the result is, whatever sA.  Moving an sW outside by a
+// power of two, and the result back, cost 4 to 12 % where the epilogue bounds, in four forms.)
 //
 // The weights are the MMA's M side (channels in TMEM lanes) and the tokens its N side
 // (columns), whatever their number: a tile is 256 channels by up to `bt` tokens on a pair
@@ -548,8 +551,8 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int at = (k >> 1) * 16 + i * 4 + (k & 1) * 2;
-                        const float2 f = mul2(make_float2(now.sw[k], now.sw[k]), sa[i]);
-                        const float2 v = mul2(make_float2((float)(int)r[at], (float)(int)r[at + 1]), f);
+                        float2 v = make_float2((float)(int)r[at], (float)(int)r[at + 1]);
+                        v = mul2(mul2(v, make_float2(now.sw[k], now.sw[k])), sa[i]);
                         __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
                         m[k] = *reinterpret_cast<uint32_t*>(&h);
                     }
@@ -679,7 +682,7 @@ int8_kernel(const __grid_constant__ CUtensorMap tmW,  // W codes [E*N][K], box 1
                     const int col = c * 4 + j;
                     const float sa = __shfl_sync(0xffffffffu, col < 32 ? sa0 : sa1, col & 31);
                     if (col < my_cols && n < s.N)
-                        Y[(size_t)(m0 + col) * s.N + n] = __float2bfloat16_rn((float)sum[j] * (sw * sa));
+                        Y[(size_t)(m0 + col) * s.N + n] = __float2bfloat16_rn((float)sum[j] * sw * sa);
                 }
             }
         }

@@ -558,9 +558,12 @@ NVFP4_API nvfp4_status gemm_nvfp4_w4a4_grouped_packed_sched_combine(
  *
  * for layers kept in 8-bit integers beside the NVFP4 ones.  a, w are signed 8-bit
  * codes, any value of -128..127; sA is one FP32 scale per token (row of A), sW one
- * per output channel (row of W).  The sum over k is an exact INT32 sum, scaled in
- * FP32 (one rounding each for sA*sW, the sum's conversion and their product) and
- * rounded once to BF16, so equal inputs give equal bits on every call.
+ * per output channel (row of W).  The sum over k is an exact INT32 sum; FP32 takes
+ * (sum * sW) * sA, with one rounding for the sum's conversion and one for each product,
+ * which is rounded once to BF16, so equal inputs give equal bits on every call.  With sW of
+ * magnitude 2^-126 .. 2^96 (or 0) nothing is lost on the way to a result within range,
+ * whatever finite sA; an sW outside meets FP32's subnormals or its largest value before
+ * sA does.
  *
  * A [M][K] and W [N][K] are row-major int8 and Y [M][N] bf16, 16-byte aligned; sA
  * [M] and sW [N] are float, 4-byte aligned.  K is a multiple of 16, 16 <= K <= 131056
