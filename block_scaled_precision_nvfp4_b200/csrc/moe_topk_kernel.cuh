@@ -320,7 +320,8 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
             b = fmaxf(fminf(a, a2), fmaxf(b, b2));
             a = fmaxf(a, a2);
         }
-        const float gs = fmaxf(group_sum ? a + b : a, -INFINITY);
+        // half the sum of two choices: that of two finite ones stays finite
+        const float gs = fmaxf(group_sum ? fmaf(0.5f, a, 0.5f * b) : a, -INFINITY);
         // groups of lower index with an equal score come first
         int better = 0;
         for (int h = 0; h < p.groups; ++h) {
@@ -333,10 +334,12 @@ moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,
             // the worst kept group and the best one left out, too close to call?
             const float lo = key_value(__reduce_min_sync(FULL, kept ? order_key(gs) : 0xFFFFFFFFu));
             const float hi = key_value(__reduce_max_sync(FULL, exists && !kept ? order_key(gs) : 0u));
-            // the terms of the largest finite sum bound every sum's error (infinite ones are exact)
+            // the terms of the largest finite sum bound every sum's error (infinite ones, of an
+            // infinite term, are exact; where the terms' magnitudes overflow, 64 bits decide)
             const float mag = key_value(__reduce_max_sync(
                 FULL, order_key(exists && fabsf(gs) < INFINITY ? fabsf(a) + (group_sum ? fabsf(b) : 0.f) : 0.f)));
-            if (lo - hi <= 2.0f * gap(mag, p.sigmoid != 0))  // false for two equal infinities
+            // (a half sum's error is at most a choice's of the size mag; false for two equal infinities)
+            if (lo - hi <= gap(mag, p.sigmoid != 0))
                 kept = group_kept_exact<V, X>(logits, bias, p, t);
         }
     }
