@@ -773,10 +773,25 @@ class GroupedSchedule:
 # their marshalling, so the plain case (tensors on the current device, no `out`, no
 # `stream`) goes through a small CPython module (csrc/host_calls.cpp).  It returns None for
 # everything else, which then takes the calls below: they do the same, and name what is
-# wrong.  Without the module (it is built against one torch version) they do all of it.
+# wrong.  Without the module of this torch and Python they do all of it.
 
 def _no_fast_call(*args):
     return None
+
+
+def _host_module():
+    """The module built for the running torch and Python, or None."""
+    from importlib import machinery, util
+    path = _build.host_calls_path()
+    if not os.path.exists(path):
+        return None
+    loader = machinery.ExtensionFileLoader(__name__ + "._host_calls", path)
+    try:
+        module = util.module_from_spec(util.spec_from_file_location(loader.name, path, loader=loader))
+        loader.exec_module(module)
+    except ImportError:
+        return None
+    return module
 
 
 class _Host:
@@ -803,9 +818,8 @@ class _Host:
         self.quantize, self.routed = lib.int8_quantize_bf16, lib.int8_quantize_bf16_routed
         self.topk = lib.nvfp4_moe_topk
         self.fast_gemm = self.fast_grouped = self.fast_quantize = self.fast_topk = _no_fast_call
-        try:
-            from . import _host_calls as fast
-        except ImportError:
+        fast = _host_module()
+        if fast is None:
             return
         fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                     for f in (self.gemm, self.grouped, self.quantize, self.routed, self.topk)))

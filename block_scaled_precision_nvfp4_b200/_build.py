@@ -12,8 +12,6 @@ LIB = os.path.join(HERE, "libnvfp4_b200.so")
 # test-only variant: same sources built with NVFP4_WAIT_TEST, whose kernels' wait
 # limit and a forced stall can be set, so that tests can make a bounded wait expire
 WAIT_TEST_LIB = os.path.join(HERE, "libnvfp4_b200_waittest.so")
-# the INT8 path's marshalling as a CPython module (host code over torch's C++ headers)
-HOST_CALLS = os.path.join(HERE, "_host_calls.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -57,12 +55,25 @@ def build_wait_test(force: bool = False) -> str:
     return _compile(WAIT_TEST_LIB, ["-DNVFP4_WAIT_TEST"], force, False)
 
 
+def host_calls_path() -> str:
+    """The INT8 path's marshalling as a CPython module (host code over torch's C++ headers).
+    It depends on the layouts of the interpreter and the torch it was built with, so its name
+    carries both: another one does not find it, and builds its own."""
+    import re
+    import sysconfig
+    import torch
+    key = "-".join((sysconfig.get_config_var("SOABI") or "", "torch", torch.__version__,
+                    (torch.version.git_version or "")[:12],
+                    "abi%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)))
+    return os.path.join(HERE, "_host_calls.%s.so" % re.sub(r"[^0-9A-Za-z+_-]", "_", key))
+
+
 def build_host_calls(force: bool = False) -> str:
-    """Compile csrc/host_calls.cpp (with g++, against the installed torch) into HOST_CALLS."""
-    src = os.path.join(CSRC, "host_calls.cpp")
+    """Compile csrc/host_calls.cpp (with g++, against the installed torch) into host_calls_path()."""
+    src, out = os.path.join(CSRC, "host_calls.cpp"), host_calls_path()
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "nvfp4.h")))
-    if not force and os.path.exists(HOST_CALLS) and os.path.getmtime(HOST_CALLS) >= newest:
-        return HOST_CALLS
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
     import sysconfig
     import torch
     base = os.path.dirname(os.path.abspath(torch.__file__))
@@ -70,7 +81,7 @@ def build_host_calls(force: bool = False) -> str:
     inc = [os.path.join(base, "include"),
            os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    tmp = HOST_CALLS + ".tmp%d" % os.getpid()
+    tmp = out + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for path in inc:
@@ -78,8 +89,8 @@ def build_host_calls(force: bool = False) -> str:
     cmd += ["-o", tmp, src, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_cuda", "-ltorch_python"]
     subprocess.check_call(cmd)
-    os.replace(tmp, HOST_CALLS)
-    return HOST_CALLS
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":
