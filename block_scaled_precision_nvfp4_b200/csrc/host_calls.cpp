@@ -18,6 +18,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cxxabi.h>
+
 #include <initializer_list>
 
 #include "../../include/nvfp4.h"
@@ -79,13 +81,17 @@ bool here(const at::Tensor* t, bool bound, int& dev, void*& stream) {
 }
 
 // `body` returns a new reference, nullptr with a Python error set, or Py_None (borrowed)
-// for the caller's own path.  No C++ exception leaves the module.
+// for the caller's own path.  No C++ exception leaves the module.  (What may pass is the
+// unwinding by which Python ends a daemon thread that asks for the lock while the interpreter
+// is being finalised: to stop it would abort the process.)
 template <typename F>
 PyObject* guarded(F&& body) {
     try {
         PyObject* r = body();
         if (r == Py_None) Py_INCREF(r);
         return r;
+    } catch (abi::__forced_unwind&) {
+        throw;
     } catch (...) {  // for example no memory: the Python path meets it again and raises it
         PyErr_Clear();
         Py_RETURN_NONE;
@@ -93,13 +99,19 @@ PyObject* guarded(F&& body) {
 }
 
 // Runs an entry point without the interpreter's lock (a launch can wait for a full queue).
+// The lock is not taken back in a destructor, which the unwinding above may not leave.
 template <typename F>
 nvfp4_status unlocked(F&& call) {
-    struct Unlock {
-        PyThreadState* state = PyEval_SaveThread();
-        ~Unlock() { PyEval_RestoreThread(state); }
-    } unlock;
-    return call();
+    PyThreadState* const state = PyEval_SaveThread();
+    nvfp4_status s;
+    try {
+        s = call();
+    } catch (...) {
+        PyEval_RestoreThread(state);
+        throw;
+    }
+    PyEval_RestoreThread(state);
+    return s;
 }
 
 PyObject* status(nvfp4_status st) { return PyLong_FromLong((long)st); }
