@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import operator
 import os
 import threading
 
@@ -862,6 +863,12 @@ def _ptr(t, dtype, shape, name, dev):
     raise ValueError(f"{name} must be on CUDA device {dev}, got {t.device}")
 
 
+def _c_int(v) -> int:
+    """v for a C int argument, which ctypes would cut to 32 bits: beyond them it becomes the
+    nearest one, and those the library refuses."""
+    return max(-2 ** 31, min(operator.index(v), 2 ** 31 - 1))
+
+
 def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
     """Y[M,N] (bf16) = sA[m] * sW[n] * A . W^T: INT8 codes A [M,K], W [N,K] with one
     float32 scale per token (sA [M]) and per output channel (sW [N]); exact INT32 sums
@@ -888,7 +895,7 @@ def gemm_int8_w8a8(A, sA, W, sW, out=None, stream=None):
         py = out.data_ptr()
     else:
         py = _ptr(out, h.bf16, (M, N), "out", dev)
-    st = h.gemm(pa, psa, pw, psw, py, M, N, K, h.stream(dev))
+    st = h.gemm(pa, psa, pw, psw, py, _c_int(M), _c_int(N), _c_int(K), h.stream(dev))
     if st:
         _err(st)
     return out
@@ -921,7 +928,7 @@ def gemm_int8_w8a8_grouped(A, sA, W, sW, offsets, out=None, stream=None):
         py = out.data_ptr()
     else:
         py = _ptr(out, h.bf16, (M, N), "out", dev)
-    st = h.grouped(pa, psa, pw, psw, po, E, M, py, N, K, h.stream(dev))
+    st = h.grouped(pa, psa, pw, psw, po, _c_int(E), _c_int(M), py, _c_int(N), _c_int(K), h.stream(dev))
     if st:
         _err(st)
     return out
@@ -946,7 +953,7 @@ def int8_quantize_bf16(x, out=None, stream=None):
     rows, K = x.shape
     px = _ptr(x, h.bf16, (rows, K), "x", dev)
     codes, scales, pc, ps = _int8_rows(h, rows, K, out, dev)
-    st = h.quantize(px, rows, K, pc, ps, h.stream(dev))
+    st = h.quantize(px, _c_int(rows), _c_int(K), pc, ps, h.stream(dev))
     if st:
         _err(st)
     return codes, scales
@@ -975,7 +982,7 @@ def int8_quantize_bf16_routed(x, dest, k=1, out=None, stream=None):
     px = _ptr(x, h.bf16, (rows, K), "x", dev)
     pd = _ptr(dest, h.i32, (rows * k,), "dest", dev)
     codes, scales, pc, ps = _int8_rows(h, rows * k, K, out, dev)
-    st = h.routed(px, rows, K, pd, k, pc, ps, h.stream(dev))
+    st = h.routed(px, _c_int(rows), _c_int(K), pd, _c_int(k), pc, ps, h.stream(dev))
     if st:
         _err(st)
     return codes, scales
@@ -1026,15 +1033,15 @@ def moe_topk(logits, k, score="softmax", bias=None, groups=1, top_groups=1, grou
     pl = _ptr(logits, dtype, (T, E), "logits", dev)
     pb = None if bias is None else _ptr(bias, h.f32, (E,), "bias", dev)
     if out is None:
-        n = k if k > 0 else 0  # a k that the library refuses
+        n = k if 0 < k <= E else 0  # the library refuses any other k
         ids, weights = h.empty((T, n), (n, 1), h.i32), h.empty((T, n), (n, 1), h.f32)
         pi, pw = ids.data_ptr(), weights.data_ptr()
     else:
         ids, weights = out
         pi = _ptr(ids, h.i32, (T, k), "ids", dev)
         pw = _ptr(weights, h.f32, (T, k), "weights", dev)
-    st = h.topk(pl, dtype is h.bf16, T, E, k, _SCORES[score], pb, groups, top_groups, group_top,
-                bool(renormalize), scale, pi, pw, h.stream(dev))
+    st = h.topk(pl, dtype is h.bf16, _c_int(T), _c_int(E), _c_int(k), _SCORES[score], pb, _c_int(groups),
+                _c_int(top_groups), _c_int(group_top), bool(renormalize), scale, pi, pw, h.stream(dev))
     if st:
         _err(st)
     return ids, weights

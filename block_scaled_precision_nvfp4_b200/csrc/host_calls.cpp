@@ -205,6 +205,7 @@ PyObject* py_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return Py_None;
         if (!here(x, g_topk, dev, st) || x->dim() != 2) return Py_None;
         const int64_t T = x->size(0), E = x->size(1);
+        if (k > E) return Py_None;  // refused there, without outputs of that size
         const bool bf16 = x->scalar_type() == at::kBFloat16;
         if (!fits(T) || !fits(E) || !is(x, bf16 ? at::kBFloat16 : at::kFloat, {T, E}, dev) ||
             (a[3] != Py_None && !is(bias, at::kFloat, {E}, dev)))
