@@ -35,3 +35,15 @@ def test_a_module_built_for_another_abi_or_python_is_not_used(monkeypatch):
     get = sysconfig.get_config_var
     monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-00-other" if n == "SOABI" else get(n))
     assert _used() == {False} and _build.host_calls_path() != built
+
+
+def test_the_build_goes_on_without_the_module(monkeypatch, capsys):
+    """The module needs torch's C++ headers; the calls do not need the module."""
+    import subprocess
+    import __graft_entry__
+
+    def fails(force=False):
+        raise subprocess.CalledProcessError(1, ["g++"])
+    monkeypatch.setattr(_build, "build_host_calls", fails)
+    __graft_entry__.build()
+    assert "host module" in capsys.readouterr().err
