@@ -19,7 +19,11 @@
 // k, and where two neighbours are closer than the bound allows, it is ranked again by
 // 64-bit choices, one list entry per lane.  Groups closer than the bound are chosen by
 // 64-bit sums; a token with more near-ties than lanes goes through 64 bits as a whole.
-// Weights are always 64-bit values of the k chosen scores, rounded once.
+// Weights are computed in 64 bits from the k chosen logits and rounded once.  Only the sum
+// that softmax weights are divided by when they are not renormalised is one of FP32
+// exponentials, added in 64 bits: it is off by at most 2 + ln E units of 2^-24 (see gap), on
+// average by less than the rounding.  (All exponentials in 64 bits are the price of the
+// whole-token path; tokens whose choices are near each other have them anyway.)
 //
 // One warp per token; a group's experts sit on `lpg` neighbouring lanes, V per lane, in
 // ascending order, so the lowest lane and the lowest slot hold the lowest index.  Few
@@ -56,12 +60,11 @@ struct Params {
 
 constexpr float FLT_LARGEST = 3.402823466e38f;
 
-// One token's logits x, scores s and choices c by the formulas in 64 bits, by its whole
-// warp; returns whether the lane's group is kept.
+// One token's scores s and choices c by the formulas in 64 bits, by its whole warp; returns
+// whether the lane's group is kept.
 template <int V, typename X>
 __device__ __forceinline__ bool exact_choices(const X* __restrict__ logits, const float* __restrict__ bias,
-                                              const Params& p, int t, double (&x)[V], double (&s)[V],
-                                              double (&c)[V]) {
+                                              const Params& p, int t, double (&s)[V], double (&c)[V]) {
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     const double NEG = -__longlong_as_double(0x7FF0000000000000ll);
@@ -69,7 +72,7 @@ __device__ __forceinline__ bool exact_choices(const X* __restrict__ logits, cons
     const int e0 = g * p.per + i0;
     const int cnt = g < p.groups ? max(0, min(V, p.per - i0)) : 0;
 
-    double xmax = NEG;
+    double x[V], xmax = NEG;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         x[v] = NEG;
@@ -134,11 +137,12 @@ __device__ __forceinline__ bool exact_choices(const X* __restrict__ logits, cons
 template <int V, typename X>
 __device__ __noinline__ bool group_kept_exact(const X* __restrict__ logits, const float* __restrict__ bias,
                                               const Params& p, int t) {
-    double x[V], s[V], c[V];
-    return exact_choices<V, X>(logits, bias, p, t, x, s, c);
+    double s[V], c[V];
+    return exact_choices<V, X>(logits, bias, p, t, s, c);
 }
 
-// The whole token in 64 bits.
+// The whole token in 64 bits, chosen with a bias (without one, experts order like their
+// logits and no near-tie arises).
 template <int V, typename X>
 __device__ __noinline__ void topk_exact(const X* __restrict__ logits, const float* __restrict__ bias,
                                         int32_t* __restrict__ ids, float* __restrict__ weights,
@@ -149,8 +153,8 @@ __device__ __noinline__ void topk_exact(const X* __restrict__ logits, const floa
     const int g = lane / p.lpg, i0 = (lane % p.lpg) * V;
     const int e0 = g * p.per + i0;
     const int cnt = g < p.groups ? max(0, min(V, p.per - i0)) : 0;
-    double x[V], s[V], c[V];
-    const bool kept = exact_choices<V, X>(logits, bias, p, t, x, s, c);
+    double s[V], c[V];
+    const bool kept = exact_choices<V, X>(logits, bias, p, t, s, c);
 
     // k rounds: the best expert left, by (choice, lowest index)
     unsigned left = kept ? (1u << cnt) - 1u : 0u;
@@ -161,9 +165,8 @@ __device__ __noinline__ void topk_exact(const X* __restrict__ logits, const floa
         int id = p.E;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const double key = bias ? c[v] : x[v];
-            if ((left >> v & 1u) && (id == p.E || key > best)) {
-                best = key;
+            if ((left >> v & 1u) && (id == p.E || c[v] > best)) {
+                best = c[v];
                 sc = s[v];
                 id = e0 + v;
             }

@@ -1630,8 +1630,8 @@ nvfp4_status nvfp4_moe_topk(const void* logits, int logits_bf16, int T, int E, i
     const int v = (per + p.lpg - 1) / p.lpg;
     const int slots = v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : v <= 8 ? 8 : 16;  // experts of a lane
     p.lanes = top_groups * ((per + slots - 1) / slots);
-    // every lane full and aligned (32, 64, .. 256 experts in 1, 2, .. groups): no lane checks
-    // its count, and logits and bias come in 16-byte pieces
+    // every lane full and aligned (128 or 256 experts in 1, 2, .. 32 groups; fewer slots have
+    // no pieces to load): no lane checks its count, and logits and bias come in 16-byte pieces
     const bool full = per == slots * p.lpg && groups * p.lpg == 32 && reinterpret_cast<uintptr_t>(bias) % 16 == 0;
     const dim3 grid((unsigned)((T + tk::WARPS - 1) / tk::WARPS));
     cudaError_t e;

@@ -624,6 +624,9 @@ NVFP4_API nvfp4_status int8_quantize_bf16_routed(const void* X_bf16, int rows, i
  *
  * Ties go to the lowest index.  Choices are compared in 64 bits (without a bias, experts
  * compare by their logits), so the ids are those of the formula and not of a rounding.
+ * Weights are computed in 64 bits and rounded once, except that softmax scores which are
+ * not renormalised may be divided by a 64-bit sum of FP32 exponentials: an error of at most
+ * (2 + ln E) 2^-24 beside the rounding's 2^-24.
  * A NaN logit counts as -Inf, +Inf as the largest finite value; a NaN choice counts as
  * -Inf.  Experts masked by -Inf (logit or bias) are chosen only when nothing else is left
  * in the kept groups; a logit of -Inf has the score 0, and a row with no logit above -Inf
