@@ -1,5 +1,8 @@
 """A process whose daemon thread is inside the host module's calls when the interpreter ends:
-Python ends such a thread by unwinding it, which must not abort the process."""
+Python ends such a thread by unwinding it, which must not abort the process.
+
+The calls are ones that the library refuses, so that nothing but the module's own handling of
+the lock is in question: torch's own calls (a loop of torch.empty on the device) abort there."""
 import os
 import subprocess
 import sys
@@ -14,13 +17,14 @@ PROGRAM = """
 import threading
 import torch
 import block_scaled_precision_nvfp4_b200 as nv
-x = torch.ones(16, 256, device="cuda", dtype=torch.bfloat16)
-nv.int8_quantize_bf16(x)
-assert nv._host().fast_quantize is not nv._no_fast_call
+a = torch.zeros(4, 24, dtype=torch.int8, device="cuda")     # K is no multiple of 16
+s = torch.ones(4, device="cuda")
+gemm = nv._host().fast_gemm
+assert gemm(a, s, a, s) == nv.Status.INVALID_ARG
 running = threading.Event()
 def loop():
-    for i in range(1000000):
-        nv.int8_quantize_bf16(x)
+    for i in range(10000000):
+        gemm(a, s, a, s)
         if i == 100:
             running.set()
 threading.Thread(target=loop, daemon=True).start()
