@@ -1,5 +1,7 @@
 """Counts that no call takes are refused as such, before anything of their size is allocated and
 without being cut to a C int on the way."""
+import gc
+
 import pytest
 import torch
 
@@ -41,17 +43,26 @@ def test_router_groups(way, kw):
     _refused(lambda: nv.moe_topk(x, 2, **kw))
 
 
-def test_more_rows_than_a_c_int(way):
+def _rows_beyond_a_c_int(monkeypatch):
     T = 2 ** 32 + 2
     x = torch.empty(T, 1, dtype=torch.bfloat16, device="cuda")
     ids = torch.empty(T, 1, dtype=torch.int32, device="cuda")
     w = torch.empty(T, 1, dtype=torch.float32, device="cuda")
     _refused(lambda: nv.moe_topk(x, 1, out=(ids, w)))
-    del x, ids
-    K = 16
-    A = torch.empty(T, K, dtype=torch.int8, device="cuda")
-    y = torch.empty(T, 1, dtype=torch.bfloat16, device="cuda")
-    one = torch.ones(1, device="cuda")
-    _refused(lambda: nv.gemm_int8_w8a8(A, w.view(-1), A[:1], one, out=y))
+    # the products' row count, as it reaches the library (K = 1 keeps the codes small; no call)
+    seen = []
+    monkeypatch.setattr(nv._host(), "gemm", lambda *a: seen.append(a[5]) or 0)
+    monkeypatch.setattr(nv._host(), "grouped", lambda *a: seen.append(a[6]) or 0)
+    A, y, one = ids.view(torch.int8)[:, :1].contiguous(), x, torch.ones(1, device="cuda")
+    nv.gemm_int8_w8a8(A, w.view(-1), A[:1], one, out=y)
     off = torch.zeros(2, dtype=torch.int32, device="cuda")
-    _refused(lambda: nv.gemm_int8_w8a8_grouped(A, w.view(-1), A[:1].view(1, 1, K), one.view(1, 1), off, out=y))
+    nv.gemm_int8_w8a8_grouped(A, w.view(-1), A[:1].view(1, 1, 1), one.view(1, 1), off, out=y)
+    assert seen == [2 ** 31 - 1] * 2          # more rows than any call takes
+
+
+def test_more_rows_than_a_c_int(monkeypatch):
+    try:
+        _rows_beyond_a_c_int(monkeypatch)
+    finally:
+        gc.collect()                          # some 50 GB
+        torch.cuda.empty_cache()
