@@ -30,10 +30,11 @@
 // bt for the tokens, against 2 bt clocks of MMA: tiles of 256 tokens are the smallest that
 // the MMA bounds.  Measured per step: 156 ns at 64 tokens, 201 at 128, 322 at 256 with
 // every SM busy.  Large products are bound by power: 4096 x 5376 x 14336 takes 163 us on
-// zeros and 199 us on random codes.  Small ones by the weights' bytes (32 rows over 8
-// experts [14336, 4096]: 72 us, 6.5 TB/s; one token at 5376 x 14336: 15.1 us, 5.1 TB/s).
-// Single SMs instead of pairs (M = 128) took 31 us for 333 tokens where pairs take 27, and
-// 78 us for 32 tokens over 8 experts where pairs take 75.
+// zeros, and on random codes 200 to 212 us in short runs, 236 to 255 us in long ones.  Small
+// ones by the weights' bytes (32 rows over 8 experts [14336, 4096]: 74 us, 6.3 TB/s; one token
+// at 5376 x 14336: 15.0 us, 5.1 TB/s).  Single SMs instead of pairs (M = 128) took 31 us for
+// 333 tokens where pairs take 27 (short runs), and 78 us for 32 tokens over 8 experts where
+// pairs take 75.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

@@ -27,9 +27,11 @@
 //
 // One warp per token; a group's experts sit on `lpg` neighbouring lanes, V per lane, in
 // ascending order, so the lowest lane and the lowest slot hold the lowest index.  Few
-// bytes, many instructions: bound by the integer and compare pipe (80 % of its rate).
-// 8192 tokens over 256 experts in 8 groups (8.9 MB, 1.4 us of HBM) take 9.7 us, 65536 of
-// them 66 us.  Everything in 64 bits took 28.8 us; selection rounds over all of a lane's
+// bytes, many instructions: bound by their issue.  8192 tokens over 256 experts in 8 groups
+// (8.9 MB, 1.4 us of HBM; 936 warp instructions a token) take 10 us, 65536 of them 66 us with
+// 81 % of the issue slots and 58 % of the integer pipe's busy (68 and 48 % at 8192 tokens,
+// which are 1.7 waves).  3001 tokens over 60 experts (480 instructions a token) take 3.7 us in
+// a graph, where 16 tokens over 8 take 1.8: half of it is one token's chain of dependent steps.  Everything in 64 bits took 28.8 us; selection rounds over all of a lane's
 // experts instead of the packed list 14.8 against 12.0 us (but for up to 2 experts per lane
 // they are the faster form: 64 experts 5.5 against 6.0 us); a whole token in 64 bits where
 // only its groups are too close, 11.7 us.
@@ -245,7 +247,7 @@ __device__ __forceinline__ void load_logits(const X* __restrict__ row, int e0, i
 }
 
 // FULL_LANES: every lane holds exactly V experts, on 16-byte (BF16: 8-byte) boundaries
-// (65536 x 256 in 8 groups: 68 us, 72 without).
+// (it took 4 us of the 72 that 65536 x 256 in 8 groups took before).
 template <int V, typename X, bool FULL_LANES>
 __global__ void __launch_bounds__(32 * WARPS, V <= 8 ? 8 : 4)
 moe_topk_kernel(const X* __restrict__ logits, const float* __restrict__ bias,

@@ -1397,7 +1397,8 @@ nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
 }
 
 // The plan with the least expected time of those that differ in token columns and in the
-// pairs per tile, by the kernel's own measured costs (B200; M x 5376 x 14336):
+// pairs per tile, by the kernel's own costs, measured in short runs (B200; M x 5376 x 14336;
+// in long ones power takes more: 333 tokens 31 us, 4096 tokens 236 to 255):
 //   a 128-byte step of K   100 + 0.87 bt ns, at least 150   (64 tokens 156, 128 201, 256 322)
 //   the weights' bytes     6.2 TB/s
 //   a tile's epilogue      0.3 us + 8.5 ns per token column, under the next tile's steps
@@ -1407,8 +1408,8 @@ nvfp4_status int8_slots(int dev, const DevInfo& info, Int8Slots& out) {
 //                          (64 tokens: 18 us on 3 pairs a tile, 21.5 unsplit)
 //   a pair that takes part 8 ns
 // A split is taken only where all of its clusters run at once, one tile each: with several
-// split tiles per cluster the exchange is not hidden (333 tokens: 43 us on 3 pairs a tile,
-// 27 unsplit).  Two steps of K per pair at least, so that each has a stage to multiply.
+// split tiles per cluster the exchange is not hidden (333 tokens, short runs: 43 us on 3 pairs
+// a tile, 27 unsplit).  Two steps of K per pair at least, so that each has a stage to multiply.
 Int8Plan int8_plan(int M, int N, int K, int E, const Int8Slots& slots) {
     namespace i8 = nvfp4::int8;
     const int steps = (K + i8::BKB - 1) / i8::BKB;

@@ -622,8 +622,9 @@ NVFP4_API nvfp4_status int8_quantize_bf16_routed(const void* X_bf16, int rows, i
  *     weights[t][j] = s of that expert, divided by the k scores' sum if `renormalize`
  *         (0 where that sum is 0), times `scale`
  *
- * Ties go to the lowest index.  Choices are compared in 64 bits (without a bias, experts
- * compare by their logits), so the ids are those of the formula and not of a rounding.
+ * Ties go to the lowest index.  Choices are compared in 64 bits (without a bias, experts,
+ * and groups by one choice, compare by their logits), so the ids are those of the formula
+ * and not of an FP32 rounding.
  * Weights are computed in 64 bits and rounded once, except that softmax scores which are
  * not renormalised may be divided by a 64-bit sum of FP32 exponentials: an error of at most
  * (2 + ln E) 2^-24 beside the rounding's 2^-24.
